@@ -12,6 +12,13 @@
  *   sd_cfg_ddim_step  classifier-free guidance fused with a deterministic DDIM latent update;
  *                     sd_cfg_dpmpp_2m_step fuses it with a DPM-Solver++(2M) update instead.
  *
+ * and two of a transformer block around its projections (diffusion transformers, text encoders,
+ * token decoders), in the order in which a block calls them:
+ *
+ *   sd_rms_norm       RMS norm with the residual's addition; sd_rms_norm_fp8 writes e4m3 values with
+ *                     scales, the input of an 8-bit projection.
+ *   sd_rope_axes      rotary positions with several axes for q and k, their heads' RMS norm fused.
+ *
  * Sources: "从零实现扩散模型推理引擎：Rust + wgpu 的 GPU 加速图像生成架构" (the Rust + wgpu engine page):
  * §1 sampling loop, §3.1 GroupNorm reduction, §3.2 flash cross-attention with online softmax, §4
  * scheduler step(model_output, timestep, sample, eta), §6 step_inplace, §7 CFG loop; and
@@ -229,6 +236,81 @@ sd_status sd_cfg_dpmpp_3m_step(const float* x, const float* eps_u, const float* 
                                const float* d_prev2, float* x_out, float* d_out, int64_t n, float w,
                                double alpha_prev2, double alpha_prev, double alpha_t, double alpha_next,
                                void* stream);
+
+/*
+ * RMS norm of rows with the residual's addition: for each of `rows` rows of `cols` values
+ *   h = x + residual (x where residual is NULL), in fp32,
+ *   residual_out = h rounded to the type,   y = h * rsqrt(mean(h^2) + eps) * weight
+ * y is formed from the unrounded h and rounded once.
+ *  dtype  : of x, residual, residual_out and y: 0 = bf16, 1 = fp16, 2 = fp32.
+ *  weight : [cols], fp32 (weight_f32 = 1) or of the type dtype (weight_f32 = 0); NULL = ones.
+ *  residual, residual_out : may be NULL; residual_out needs residual.
+ *  *_stride : elements from one row to the next, >= cols. Rows are contiguous. Any alignment of the
+ *           type is accepted; 16-byte aligned rows of whole 16-byte packs take the vectorised path.
+ *  y and residual_out may each equal x or residual exactly (pointer and stride, in place); any other
+ *           overlap of an output with an input or with another output is SD_ERR_INVALID_ARG.
+ *  eps    : finite and >= 0.  rows < 2^31, cols <= 2^30.
+ */
+sd_status sd_rms_norm(const void* x, const void* residual, const void* weight, void* y, void* residual_out,
+                      int64_t rows, int64_t cols, int64_t x_stride, int64_t residual_stride, int64_t y_stride,
+                      int64_t residual_out_stride, float eps, int dtype, int weight_f32, void* stream);
+
+/*
+ * sd_rms_norm with y in 8 bits: each block of `block` columns of a row (the last may be shorter), or
+ * the whole row for block = 0, has the scale s = max(max|y| / 448, 2^-126) and the e4m3 values
+ * q = y / s (formed as y * (1 / s) in fp32, round to nearest even). q * s stands for y. A NaN in a
+ * block makes its scale and values NaN.
+ *  y      : e4m3 bytes, y_stride bytes from row to row; must not overlap an input.
+ *  scales : fp32 [rows, ceil(cols / block)], or [rows] for block = 0, contiguous.
+ *  block  : 0, 32, 64 or 128 (others SD_ERR_UNSUPPORTED).
+ * Everything else as in sd_rms_norm.
+ */
+sd_status sd_rms_norm_fp8(const void* x, const void* residual, const void* weight, void* y, float* scales,
+                          void* residual_out, int64_t rows, int64_t cols, int64_t x_stride, int64_t residual_stride,
+                          int64_t y_stride, int64_t residual_out_stride, float eps, int dtype, int weight_f32,
+                          int block, void* stream);
+
+/*
+ * Rotary positions with several axes (a token's time, height and width; its place in a text) for the
+ * queries and keys of one attention, with the RMS norm of each head before it. For each head x of dh
+ * columns of token (b, t):
+ *   y = x * rsqrt(mean(x^2) + eps) * weight     (y = x where the weight is NULL), in fp32,
+ * and pair m of the axis a that holds it, (u, v) -> (u cos - v sin, u sin + v cos) with the angle
+ *   2 pi * frac(positions[b, t, a] * freqs[m] / 2^64),
+ * rounded once. Columns behind the axes' columns are normalised but not turned. With -freqs the
+ * rotation is undone, which is also its gradient's form.
+ *  q, k, q_out, k_out : [B, L, heads, dh] and [B, L, kv_heads, dh] views of the type dtype (0 = bf16,
+ *           1 = fp16, 2 = fp32) with strides {batch, token, head} in elements and contiguous columns,
+ *           so that both layouts of sd_attention and the rows of a fused projection will do; 16-byte
+ *           aligned, strides multiples of 16 bytes (SD_ERR_MISALIGNED). heads or kv_heads may be 0:
+ *           that tensor is then not looked at. q_out may be q and k_out may be k exactly (in place);
+ *           any other overlap of an output is SD_ERR_INVALID_ARG.
+ *  dh     : a multiple of 8 from 8 to 256.
+ *  axes, axis_dims : 1 to 4 axes of an even number of columns each (0 allowed), together a multiple of
+ *           8 and at most dh. Axis a holds the pairs behind those of axis a - 1.
+ *  pairs  : 0 = pair m is columns (2m, 2m + 1); 1 = columns (m, m + rot / 2), rot the axes' columns.
+ *  freqs  : uint64 [rot / 2], the fraction of a turn per position in units of 2^-64 (modulo 1: a
+ *           negative frequency is its two's complement).
+ *  positions : int32 [B, L, axes], positions_batch_stride elements from batch to batch; 0 shares one
+ *           [L, axes] between the batches.
+ *  q_weight, k_weight : fp32 [dh], 16-byte aligned, or NULL (that tensor is not normalised).
+ *  eps    : finite and >= 0.
+ */
+typedef struct sd_rope_args {
+  const void *q, *k;
+  void *q_out, *k_out;
+  const float *q_weight, *k_weight;
+  const int32_t* positions;
+  const uint64_t* freqs;
+  int64_t B, L, heads, kv_heads, dh;
+  int64_t q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];
+  int64_t positions_batch_stride;
+  int32_t axis_dims[4];
+  int32_t axes, pairs, dtype;
+  float eps;
+} sd_rope_args;
+
+sd_status sd_rope_axes(const sd_rope_args* args, void* stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* sd_status_string(sd_status status);

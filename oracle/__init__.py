@@ -9,6 +9,9 @@ Plain, slow, fp64 numpy restatements of what the CUDA library computes:
                       (eta = 0), plus the scaled-linear noise schedule      -> oracle/ddim.py
 * ``cfg_dpmpp_2m_step`` guidance followed by a DPM-Solver++(2M) multistep update, plus
                       Karras sigmas                                        -> oracle/dpmpp.py
+* ``rms_norm``        RMS norm of rows with the residual's addition; scales of its e4m3 form
+                                                                           -> oracle/rms_norm.py
+* ``rope_axes``       per-head RMS norm and rotary positions with several axes -> oracle/rope.py
 
 Sources, cited in each function by page title and section:
 
@@ -31,9 +34,12 @@ from .ddim import (cfg, ddim_step, cfg_ddim_step, scaled_linear_betas, alphas_cu
 from .dpmpp import (lam, data_prediction, dpmpp_2m_step, cfg_dpmpp_2m_step, dpmpp_3m_step, cfg_dpmpp_3m_step,
                     karras_sigmas, alpha_bar_of_sigma,
                     sd_sigma_range, dpmpp_2m_schedule, cfg_dpmpp_2m_loop, dpmpp_3m_schedule, cfg_dpmpp_3m_loop)
+from .rms_norm import rms_norm, block_scales, spread_scales
+from .rope import rope_axes
 
 __all__ = ["attention", "attention_rows", "softmax_weights", "group_norm", "group_norm_silu", "group_stats",
            "silu", "cfg", "ddim_step", "cfg_ddim_step", "scaled_linear_betas", "alphas_cumprod", "ddim_timesteps",
            "ddim_schedule", "cfg_ddim_loop", "lam", "data_prediction", "dpmpp_2m_step", "cfg_dpmpp_2m_step",
            "dpmpp_3m_step", "cfg_dpmpp_3m_step", "karras_sigmas", "alpha_bar_of_sigma", "sd_sigma_range", "dpmpp_2m_schedule", "cfg_dpmpp_2m_loop",
-           "dpmpp_3m_schedule", "cfg_dpmpp_3m_loop"]
+           "dpmpp_3m_schedule", "cfg_dpmpp_3m_loop",
+           "rms_norm", "block_scales", "spread_scales", "rope_axes"]

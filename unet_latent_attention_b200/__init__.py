@@ -10,6 +10,12 @@ CPU fallback: if the library is missing or the tensors are not on a CUDA device,
     sd_cfg_ddim_step(x, eps_u, eps_c, w, alpha_t, alpha_prev, out=None)
     sd_cfg_ddim_step_from_noise_pred(x, noise_pred, w, alpha_t, alpha_prev, out=None)
     sd_cfg_dpmpp_2m_step(x, eps_u, eps_c, d_prev, w, alpha_prev, alpha_t, alpha_next, order, out=None, d_out=None)
+
+and, for transformer blocks, in the order in which a block calls them:
+
+    sd_rms_norm(x, weight, eps=1e-6, residual=None)                  -> y or (y, residual)
+    sd_rms_norm_fp8(x, weight, eps=1e-6, residual=None, block=0)     -> (y, scales) or (y, scales, residual)
+    sd_rope_axes(q, k, positions, freqs, axis_dims, ...)             -> (q, k)     (freqs: rope_frequencies)
 """
 from __future__ import annotations
 
@@ -18,6 +24,7 @@ import math
 import os
 import re
 
+from .rope import rope_frequencies  # noqa: F401
 from .schedule import (ddim_schedule, dpmpp_2m_schedule, dpmpp_3m_schedule, karras_alpha_bars,  # noqa: F401
                        scaled_linear_alphas_cumprod)
 
@@ -36,6 +43,14 @@ class SDError(RuntimeError):
     def __init__(self, func: str, status: int, detail: str):
         self.status = status
         super().__init__(f"{func}: {STATUS_NAMES.get(status, status)}: {detail}")
+
+
+class _RopeArgs(ctypes.Structure):  # sd_rope_args
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "q_out", "k_out", "q_weight", "k_weight", "positions", "freqs")]
+                + [(n, ctypes.c_int64) for n in ("B", "L", "heads", "kv_heads", "dh")]
+                + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
+                + [("positions_batch_stride", ctypes.c_int64), ("axis_dims", ctypes.c_int32 * 4)]
+                + [(n, ctypes.c_int32) for n in ("axes", "pairs", "dtype")] + [("eps", ctypes.c_float)])
 
 
 _lib = None
@@ -58,11 +73,14 @@ def lib() -> ctypes.CDLL:
         L.sd_cfg_ddim_step.argtypes = [vp, vp, vp, vp, i64, f32, f64, f64, vp]
         L.sd_cfg_dpmpp_2m_step.argtypes = [vp, vp, vp, vp, vp, vp, i64, f32, f64, f64, f64, c_int, vp]
         L.sd_cfg_dpmpp_3m_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, f32, f64, f64, f64, f64, vp]
+        L.sd_rms_norm.argtypes = [vp] * 5 + [i64] * 6 + [f32, c_int, c_int, vp]
+        L.sd_rms_norm_fp8.argtypes = [vp] * 6 + [i64] * 6 + [f32, c_int, c_int, c_int, vp]
+        L.sd_rope_axes.argtypes = [ctypes.POINTER(_RopeArgs), vp]
         L.sd_device_status.argtypes = [vp, c_int]
         L.sd_debug_set_fault.argtypes = [c_int]
         L.sd_debug_set_fault.restype = None
         for f in ("sd_group_norm", "sd_group_norm_silu", "sd_attention", "sd_attention_noalloc", "sd_attention_f16",
-                  "sd_attention_layout",
+                  "sd_attention_layout", "sd_rms_norm", "sd_rms_norm_fp8", "sd_rope_axes",
                   "sd_cfg_ddim_step",
                   "sd_cfg_dpmpp_2m_step", "sd_cfg_dpmpp_3m_step", "sd_device_status"):
             getattr(L, f).restype = c_int
@@ -268,6 +286,210 @@ def sd_cfg_dpmpp_3m_step(x, eps_u, eps_c, d_prev, d_prev2, w: float, alpha_prev2
         x.data_ptr(), eps_u.data_ptr(), eps_c.data_ptr(), d_prev.data_ptr(), d_prev2.data_ptr(), out.data_ptr(),
         d_out.data_ptr(), x.numel(), w, alpha_prev2, alpha_prev, alpha_t, alpha_next, _stream(x)))
     return out, d_out
+
+
+def _same_cuda_device(*ts):
+    """The device of CUDA tensors that may be strided views; None entries are skipped."""
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("sd kernels run on CUDA tensors only (no CPU fallback)")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("all tensors must be on one CUDA device")
+    return dev
+
+
+def _call(name, dev, *args) -> None:
+    """One library call on the current stream of ``dev``, with ``dev`` as the current device."""
+    import torch
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != SD_OK:
+        _check(name, st)
+
+
+def _rows(t, name):
+    """(number of rows, elements between rows) of a tensor whose last dimension is contiguous."""
+    C = t.shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // C if C else 0), C
+    if C > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    n, step = 1, None
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if step is None:
+            step = stride
+        elif stride != step * n:
+            raise ValueError(f"the rows of {name} must be equally far apart")
+        n *= size
+    return (n if t.numel() else 0), (C if step is None else step)
+
+
+_DTYPE_CODES = {}
+
+
+def _dtype_code(t, func):
+    if not _DTYPE_CODES:
+        import torch
+        _DTYPE_CODES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{func} takes bf16, fp16 or fp32 tensors")
+    return code
+
+
+def _rms(func, x, weight, eps, residual, out, residual_out, scales, block):
+    import torch
+    code = _dtype_code(x, func)
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    C = x.shape[-1]
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
+        raise ValueError("residual must have the shape and type of x")
+    if residual_out is not None and residual is None:
+        raise ValueError("residual_out needs residual")
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if residual_out is not None and (residual_out.shape != x.shape or residual_out.dtype != x.dtype):
+        raise ValueError("residual_out must have the shape and type of x")
+    wf32 = 1
+    if weight is not None:
+        if weight.shape != (C,) or weight.dtype not in (torch.float32, x.dtype) or not weight.is_contiguous():
+            raise ValueError("weight must be [C], contiguous, fp32 or of the type of x")
+        wf32 = int(weight.dtype == torch.float32)
+    dev = _same_cuda_device(x, weight, residual, out, residual_out, scales)
+    rows, xs = _rows(x, "x")
+    rs = _rows(residual, "residual")[1] if residual is not None else C
+    ros = _rows(residual_out, "residual_out")[1] if residual_out is not None else C
+    ys = _rows(out, "out")[1]
+    ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+    if scales is None:
+        _call(func, dev, x.data_ptr(), ptr(residual), ptr(weight), out.data_ptr(), ptr(residual_out), rows, C, xs, rs, ys,
+              ros, eps, code, wf32)
+    else:
+        _call(func, dev, x.data_ptr(), ptr(residual), ptr(weight), out.data_ptr(), scales.data_ptr(), ptr(residual_out),
+              rows, C, xs, rs, ys, ros, eps, code, wf32, block)
+    return residual_out
+
+
+def sd_rms_norm(x, weight=None, eps: float = 1e-6, residual=None, out=None, residual_out=None):
+    """RMS norm over the last dimension of ``x`` (bf16, fp16 or fp32), or of ``x + residual``.
+
+    ``weight`` is [C] in fp32 or the type of x (None: ones). Returns y, or (y, residual_out) with
+    residual_out = x + residual where a residual is given. ``out`` and ``residual_out`` may be ``x`` or
+    ``residual`` (in place); rows may be strided, columns are contiguous."""
+    import torch
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have the shape and type of x")
+    ro = _rms("sd_rms_norm", x, weight, float(eps), residual, out, residual_out, None, 0)
+    return out if ro is None else (out, ro)
+
+
+def sd_rms_norm_fp8(x, weight=None, eps: float = 1e-6, residual=None, block: int = 0, out=None, scales=None,
+                    residual_out=None):
+    """sd_rms_norm with an e4m3 output: y = out * scale, a scale for each ``block`` columns of a row (32, 64
+    or 128; 0: one a row). Returns (out, scales) or (out, scales, residual_out); scales is fp32
+    [..., ceil(C / block)] ([..., 1] for block 0)."""
+    import torch
+    if block not in (0, 32, 64, 128):
+        raise ValueError("block must be 0, 32, 64 or 128")
+    C = x.shape[-1] if x.dim() else 0
+    shape = (*x.shape[:-1], -(-C // block) if block else 1)
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    elif out.shape != x.shape or out.dtype != torch.float8_e4m3fn:
+        raise ValueError("out must have the shape of x and type float8_e4m3fn")
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+    elif scales.shape != shape or scales.dtype != torch.float32 or not scales.is_contiguous():
+        raise ValueError(f"scales must be contiguous fp32 {list(shape)}")
+    ro = _rms("sd_rms_norm_fp8", x, weight, float(eps), residual, out, residual_out, scales, block)
+    return (out, scales) if ro is None else (out, scales, ro)
+
+
+def _strides(t, blhd, name):
+    """{batch, token, head} strides of a 4-D view with contiguous columns."""
+    s = t.stride()
+    if s[3] != 1 and t.shape[3] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return (s[0], s[1], s[2]) if blhd else (s[0], s[2], s[1])
+
+
+def sd_rope_axes(q, k, positions, freqs, axis_dims, pairs: str = "interleaved", layout: str = "blhd", q_weight=None,
+                 k_weight=None, eps: float = 1e-6, q_out=None, k_out=None):
+    """Rotary positions with several axes for ``q`` and ``k`` (or None), after the RMS norm of each head where
+    ``q_weight`` / ``k_weight`` (fp32 [dh]) is given; returns (q_out, k_out).
+
+    q and k are [B, L, heads, dh] (layout "blhd") or [B, heads, L, dh] ("bhld"), bf16, fp16 or fp32, and may
+    be strided views (a fused projection's rows). ``positions`` is int32 [B, L, axes] or [L, axes],
+    ``axis_dims`` the columns of each axis and ``freqs`` the table of ``rope_frequencies``. ``pairs`` is
+    "interleaved" (columns 2m, 2m + 1) or "half" (m, m + rot / 2). ``q_out`` may be ``q``, ``k_out`` ``k``."""
+    import torch
+    if pairs not in ("interleaved", "half"):
+        raise ValueError("pairs must be 'interleaved' or 'half'")
+    if layout not in ("bhld", "blhd"):
+        raise ValueError("layout must be 'bhld' or 'blhd'")
+    code = _dtype_code(q, "sd_rope_axes")
+    blhd = layout == "blhd"
+    if q.dim() != 4:
+        raise ValueError("q must be 4-D")
+    B, L, H = (q.shape[0], q.shape[1], q.shape[2]) if blhd else (q.shape[0], q.shape[2], q.shape[1])
+    dh = q.shape[3]
+    axes = len(axis_dims)
+    if not 1 <= axes <= 4:
+        raise ValueError("1 to 4 axes")
+    if k is not None and (k.dim() != 4 or k.dtype != q.dtype or k.shape[0] != B or k.shape[1 if blhd else 2] != L
+                          or k.shape[3] != dh):
+        raise ValueError("k must match q in type, batch, length and head dim")
+    if positions.dtype != torch.int32 or tuple(positions.shape) not in ((B, L, axes), (L, axes)) or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous int32 [B, L, axes] or [L, axes]")
+    if freqs.dtype != torch.int64 or freqs.shape != (sum(axis_dims) // 2,) or not freqs.is_contiguous():
+        raise ValueError("freqs must be int64 [sum(axis_dims) / 2]")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != torch.float32 or w.shape != (dh,) or not w.is_contiguous()):
+            raise ValueError("q_weight and k_weight must be contiguous fp32 [dh]")
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+    if q_out.shape != q.shape or q_out.dtype != q.dtype:
+        raise ValueError("q_out must have the shape and type of q")
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out needs k")
+    else:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
+        if k_out.shape != k.shape or k_out.dtype != k.dtype:
+            raise ValueError("k_out must have the shape and type of k")
+    dev = _same_cuda_device(q, k, positions, freqs, q_weight, k_weight, q_out, k_out)
+    a = _RopeArgs()
+    a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
+    a.q_stride, a.q_out_stride = _strides(q, blhd, "q"), _strides(q_out, blhd, "q_out")
+    if k is not None:
+        a.k, a.k_out = k.data_ptr(), k_out.data_ptr()
+        a.k_stride, a.k_out_stride = _strides(k, blhd, "k"), _strides(k_out, blhd, "k_out")
+        a.kv_heads = k.shape[2 if blhd else 1]
+    if q_weight is not None:
+        a.q_weight = q_weight.data_ptr()
+    if k_weight is not None:
+        a.k_weight = k_weight.data_ptr()
+    a.positions, a.freqs = positions.data_ptr(), freqs.data_ptr()
+    a.B, a.L, a.heads, a.dh = B, L, H, dh
+    a.positions_batch_stride = L * axes if positions.dim() == 3 else 0
+    for i, d in enumerate(axis_dims):
+        a.axis_dims[i] = d
+    a.axes, a.pairs, a.dtype, a.eps = axes, int(pairs == "half"), code, eps
+    _call("sd_rope_axes", dev, a)
+    return q_out, k_out
 
 
 def sd_device_status(stream=None, reset: bool = True) -> int:
