@@ -12,12 +12,14 @@
  *   sd_cfg_ddim_step  classifier-free guidance fused with a deterministic DDIM latent update;
  *                     sd_cfg_dpmpp_2m_step fuses it with a DPM-Solver++(2M) update instead.
  *
- * and two of a transformer block around its projections (diffusion transformers, text encoders,
+ * and three of a transformer block around its projections (diffusion transformers, text encoders,
  * token decoders), in the order in which a block calls them:
  *
  *   sd_rms_norm       RMS norm with the residual's addition; sd_rms_norm_fp8 writes e4m3 values with
  *                     scales, the input of an 8-bit projection.
  *   sd_rope_axes      rotary positions with several axes for q and k, their heads' RMS norm fused.
+ *   sd_attention_masked  attention with length, causal, prefix and document masks, a tanh cap and a
+ *                     bias by distance, for grouped heads, strided tensors and single tokens.
  *
  * Sources: "从零实现扩散模型推理引擎：Rust + wgpu 的 GPU 加速图像生成架构" (the Rust + wgpu engine page):
  * §1 sampling loop, §3.1 GroupNorm reduction, §3.2 flash cross-attention with online softmax, §4
@@ -311,6 +313,51 @@ typedef struct sd_rope_args {
 } sd_rope_args;
 
 sd_status sd_rope_axes(const sd_rope_args* args, void* stream);
+
+/*
+ * Attention with masks, a tanh cap and a bias by distance. The queries and keys of one sequence s are
+ * numbered i = 0, 1, ... and j = 0, 1, ...; query i stands at key position p = start_s + i:
+ *   t_ij = scale * q_i . k_j;   with a cap: t = cap * tanh(t / cap);
+ *   with a bias: t += bias[h, clamp(j - p, -bias_radius, bias_radius) + bias_radius];
+ *   key j is seen if j < len_s and (not causal, or j <= p, or j < prefix_s);
+ *   o_i = sum_j softmax_j(t_ij over the seen keys) v_j, and 0 where no key is seen (or every seen
+ *   t_ij is -infinity).
+ * Values of keys that a query does not see have no influence on it, infinities and NaN included.
+ * Batched (offsets NULL): sequence s is batch row s with all Lq queries; len_s = kv_lens[s] or Lk;
+ *   start_s = q_starts[s] or Lk - Lq.
+ * Packed documents (B = 1, q_offsets and k_offsets given, kv_lens NULL): document s has the queries
+ *   q_offsets[s] .. q_offsets[s + 1] and the keys k_offsets[s] .. k_offsets[s + 1] (both ascending);
+ *   start_s = q_starts[s] or its number of keys minus its number of queries. Rows of o in no document
+ *   are left as they were.
+ *  q, o   : [B, Lq, heads, dh] views, k, v: [B, Lk, kv_heads, dh] views, bf16 (dtype 0) or fp16 (1),
+ *           strides {batch, token, head} in elements, columns contiguous; 16-byte aligned, strides
+ *           multiples of 8 elements (SD_ERR_MISALIGNED). Query head h reads key head
+ *           h / (heads / kv_heads); kv_heads divides heads. o must not overlap q, k or v, nor fold
+ *           onto itself.
+ *  dh     : a multiple of 8 from 8 to 160.  Lq, Lk < 2^30, B * heads < 2^31. Lk = 0 gives zeros.
+ *  scale  : finite and >= 0.  cap: 0 = none, else in [1e-6, 1e30].
+ *  bias   : fp32 [heads, 2 * bias_radius + 1] or NULL; 0 <= bias_radius < 2^29. Values may be
+ *           -infinity, or the lowest of a type; +infinity and NaN spread over their rows.
+ *  causal : 0 or 1.  kv_lens, q_starts, prefix_lens: int32, one per sequence, or NULL (prefix 0).
+ *           Lengths beyond the tensors are clamped to them, starts to +-2^30. prefix_lens needs causal.
+ *  q_offsets, k_offsets : int32 [docs + 1]; docs >= 1.
+ * No workspace: a call with few query rows splits the keys over the CTAs of a cluster, which join
+ * their parts through distributed shared memory. Concurrent calls and captured graphs share nothing.
+ */
+typedef struct sd_attention_masked_args {
+  const void *q, *k, *v;
+  void* o;
+  const float* bias;
+  const int32_t *kv_lens, *q_starts, *prefix_lens;
+  const int32_t *q_offsets, *k_offsets;
+  int64_t B, heads, kv_heads, Lq, Lk, dh;
+  int64_t q_stride[3], k_stride[3], v_stride[3], o_stride[3];
+  int64_t bias_radius, docs;
+  int32_t causal, dtype;
+  float scale, cap;
+} sd_attention_masked_args;
+
+sd_status sd_attention_masked(const sd_attention_masked_args* args, void* stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* sd_status_string(sd_status status);

@@ -12,6 +12,8 @@ Plain, slow, fp64 numpy restatements of what the CUDA library computes:
 * ``rms_norm``        RMS norm of rows with the residual's addition; scales of its e4m3 form
                                                                            -> oracle/rms_norm.py
 * ``rope_axes``       per-head RMS norm and rotary positions with several axes -> oracle/rope.py
+* ``attention_masked`` attention with length, causal, prefix and document masks, a tanh cap and a bias
+                      by distance                                          -> oracle/attention_masked.py
 
 Sources, cited in each function by page title and section:
 
@@ -36,10 +38,11 @@ from .dpmpp import (lam, data_prediction, dpmpp_2m_step, cfg_dpmpp_2m_step, dpmp
                     sd_sigma_range, dpmpp_2m_schedule, cfg_dpmpp_2m_loop, dpmpp_3m_schedule, cfg_dpmpp_3m_loop)
 from .rms_norm import rms_norm, block_scales, spread_scales
 from .rope import rope_axes
+from .attention_masked import attention_masked, seen_keys
 
 __all__ = ["attention", "attention_rows", "softmax_weights", "group_norm", "group_norm_silu", "group_stats",
            "silu", "cfg", "ddim_step", "cfg_ddim_step", "scaled_linear_betas", "alphas_cumprod", "ddim_timesteps",
            "ddim_schedule", "cfg_ddim_loop", "lam", "data_prediction", "dpmpp_2m_step", "cfg_dpmpp_2m_step",
            "dpmpp_3m_step", "cfg_dpmpp_3m_step", "karras_sigmas", "alpha_bar_of_sigma", "sd_sigma_range", "dpmpp_2m_schedule", "cfg_dpmpp_2m_loop",
            "dpmpp_3m_schedule", "cfg_dpmpp_3m_loop",
-           "rms_norm", "block_scales", "spread_scales", "rope_axes"]
+           "rms_norm", "block_scales", "spread_scales", "rope_axes", "attention_masked", "seen_keys"]

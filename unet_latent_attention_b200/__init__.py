@@ -16,6 +16,7 @@ and, for transformer blocks, in the order in which a block calls them:
     sd_rms_norm(x, weight, eps=1e-6, residual=None)                  -> y or (y, residual)
     sd_rms_norm_fp8(x, weight, eps=1e-6, residual=None, block=0)     -> (y, scales) or (y, scales, residual)
     sd_rope_axes(q, k, positions, freqs, axis_dims, ...)             -> (q, k)     (freqs: rope_frequencies)
+    sd_attention_masked(q, k, v, causal=, cap=, bias=, kv_lens=, q_offsets=, ...)
 """
 from __future__ import annotations
 
@@ -53,6 +54,16 @@ class _RopeArgs(ctypes.Structure):  # sd_rope_args
                 + [(n, ctypes.c_int32) for n in ("axes", "pairs", "dtype")] + [("eps", ctypes.c_float)])
 
 
+class _AttentionMaskedArgs(ctypes.Structure):  # sd_attention_masked_args
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "bias", "kv_lens", "q_starts", "prefix_lens",
+                                                "q_offsets", "k_offsets")]
+                + [(n, ctypes.c_int64) for n in ("B", "heads", "kv_heads", "Lq", "Lk", "dh")]
+                + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride", "o_stride")]
+                + [(n, ctypes.c_int64) for n in ("bias_radius", "docs")]
+                + [(n, ctypes.c_int32) for n in ("causal", "dtype")]
+                + [(n, ctypes.c_float) for n in ("scale", "cap")])
+
+
 _lib = None
 
 
@@ -76,11 +87,12 @@ def lib() -> ctypes.CDLL:
         L.sd_rms_norm.argtypes = [vp] * 5 + [i64] * 6 + [f32, c_int, c_int, vp]
         L.sd_rms_norm_fp8.argtypes = [vp] * 6 + [i64] * 6 + [f32, c_int, c_int, c_int, vp]
         L.sd_rope_axes.argtypes = [ctypes.POINTER(_RopeArgs), vp]
+        L.sd_attention_masked.argtypes = [ctypes.POINTER(_AttentionMaskedArgs), vp]
         L.sd_device_status.argtypes = [vp, c_int]
         L.sd_debug_set_fault.argtypes = [c_int]
         L.sd_debug_set_fault.restype = None
         for f in ("sd_group_norm", "sd_group_norm_silu", "sd_attention", "sd_attention_noalloc", "sd_attention_f16",
-                  "sd_attention_layout", "sd_rms_norm", "sd_rms_norm_fp8", "sd_rope_axes",
+                  "sd_attention_layout", "sd_rms_norm", "sd_rms_norm_fp8", "sd_rope_axes", "sd_attention_masked",
                   "sd_cfg_ddim_step",
                   "sd_cfg_dpmpp_2m_step", "sd_cfg_dpmpp_3m_step", "sd_device_status"):
             getattr(L, f).restype = c_int
@@ -490,6 +502,88 @@ def sd_rope_axes(q, k, positions, freqs, axis_dims, pairs: str = "interleaved", 
     a.axes, a.pairs, a.dtype, a.eps = axes, int(pairs == "half"), code, eps
     _call("sd_rope_axes", dev, a)
     return q_out, k_out
+
+
+def sd_attention_masked(q, k, v, scale: float | None = None, layout: str = "bhld", causal: bool = False, cap: float = 0.0,
+                        bias=None, kv_lens=None, q_starts=None, prefix_lens=None, q_offsets=None, k_offsets=None,
+                        out=None):
+    """Attention with masks, a tanh cap of the scores and a bias by distance.
+
+    q [B, heads, Lq, dh] and k, v [B, kv_heads, Lk, dh] (layout "bhld") or [B, L, heads, dh] ("blhd"), all
+    bf16 or all fp16, possibly strided views; kv_heads divides heads; dh is a multiple of 8 up to 160; scale
+    defaults to 1/sqrt(dh). Query i of a sequence stands at key position start + i.
+
+    causal      a query sees keys up to its own position (and the first ``prefix_lens`` keys)
+    cap         > 0: scores become cap * tanh(score / cap)
+    bias        fp32 [heads, 2 R + 1]: score += bias[h, clamp(j - position, -R, R) + R]
+    kv_lens     int32 [B]: keys behind a sequence's length are not seen (default Lk)
+    q_starts    int32 [B or docs]: position of the first query (default Lk - Lq, or a document's keys - queries)
+    q_offsets, k_offsets   int32 [docs + 1]: B = 1 holds packed documents; each sees only itself, and rows of
+                ``out`` in no document are left as they were (0 where out is not given)
+
+    A query that sees no key gets 0. Values of keys it does not see never reach it, NaN included."""
+    import torch
+    code = _dtype_code(q, "sd_attention_masked")
+    if code == 2 or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("sd_attention_masked takes q, k, v all bf16 or all fp16")
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k, v must be 4-D")
+    if layout not in ("bhld", "blhd"):
+        raise ValueError("layout must be 'bhld' or 'blhd'")
+    blhd = layout == "blhd"
+    B, dh = q.shape[0], q.shape[3]
+    Lq, H = (q.shape[1], q.shape[2]) if blhd else (q.shape[2], q.shape[1])
+    Lk, KV = (k.shape[1], k.shape[2]) if blhd else (k.shape[2], k.shape[1])
+    if k.shape[0] != B or k.shape[3] != dh or v.shape != k.shape:
+        raise ValueError("k and v must match each other, and q in batch and head dim")
+    if (q_offsets is None) != (k_offsets is None):
+        raise ValueError("q_offsets and k_offsets go together")
+    docs = 0
+    if q_offsets is not None:
+        if kv_lens is not None:
+            raise ValueError("packed documents have their lengths from k_offsets: kv_lens must be None")
+        if B != 1:
+            raise ValueError("packed documents need a batch of 1")
+        docs = q_offsets.numel() - 1
+        if docs < 1 or k_offsets.numel() != docs + 1:
+            raise ValueError("q_offsets and k_offsets must both be [docs + 1], docs >= 1")
+    n_seq = docs or B
+    for name, t, n in (("kv_lens", kv_lens, n_seq), ("q_starts", q_starts, n_seq), ("prefix_lens", prefix_lens, n_seq),
+                       ("q_offsets", q_offsets, docs + 1), ("k_offsets", k_offsets, docs + 1)):
+        if t is not None and (t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous int32 [{n}]")
+    if prefix_lens is not None and not causal:
+        raise ValueError("prefix_lens needs causal")
+    radius = 0
+    if bias is not None:
+        if (bias.dtype != torch.float32 or bias.dim() != 2 or bias.shape[0] != H or bias.shape[1] % 2 != 1
+                or not bias.is_contiguous()):
+            raise ValueError("bias must be contiguous fp32 [heads, 2 R + 1]")
+        radius = bias.shape[1] // 2
+    if out is None:
+        make = torch.zeros if docs else torch.empty
+        out = make(q.shape, dtype=q.dtype, device=q.device)
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have the shape and type of q")
+    dev = _same_cuda_device(q, k, v, out, bias, kv_lens, q_starts, prefix_lens, q_offsets, k_offsets)
+    a = _AttentionMaskedArgs()
+    a.q, a.k, a.v, a.o = q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr()
+    a.q_stride, a.k_stride = _strides(q, blhd, "q"), _strides(k, blhd, "k")
+    a.v_stride, a.o_stride = _strides(v, blhd, "v"), _strides(out, blhd, "out")
+    a.B, a.heads, a.kv_heads, a.Lq, a.Lk, a.dh = B, H, KV, Lq, Lk, dh
+    if bias is not None:
+        a.bias, a.bias_radius = bias.data_ptr(), radius
+    if kv_lens is not None:
+        a.kv_lens = kv_lens.data_ptr()
+    if q_starts is not None:
+        a.q_starts = q_starts.data_ptr()
+    if prefix_lens is not None:
+        a.prefix_lens = prefix_lens.data_ptr()
+    if docs:
+        a.q_offsets, a.k_offsets, a.docs = q_offsets.data_ptr(), k_offsets.data_ptr(), docs
+    a.causal, a.dtype, a.scale, a.cap = int(bool(causal)), code, 1.0 / math.sqrt(dh) if scale is None else scale, cap
+    _call("sd_attention_masked", dev, a)
+    return out
 
 
 def sd_device_status(stream=None, reset: bool = True) -> int:

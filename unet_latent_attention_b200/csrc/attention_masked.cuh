@@ -1,0 +1,705 @@
+// Masked attention on sm_100a (sd_attention_masked): the kernel, shared by the translation units that
+// instantiate it per head size.
+//
+//   t_ij = scale q_i . k_j  (cap * tanh(t / cap))  (+ bias[h, clamp(distance)]);  o_i = softmax_j(t_ij) v_j
+//
+// Every mask of the operator (length, causal, prefix, document) leaves one interval of keys [lo_i, hi_i)
+// per query, and both ends grow with i. So a tile of queries needs the key tiles from lo of its first
+// row to hi of its last one, and only those that reach past lo of the last or hi of the first row need
+// element masks: the others run as if there were no mask.
+//
+// A CTA owns NQ tiles of 128 query rows of one (batch, head) and streams the key tiles of both once.
+//  * warp 0: TMA producer of Q and of the K/V ring (rows past the end read as zeros).
+//  * warps 1, 2: one thread each issues the tcgen05 work of one query tile: S = Q K^T into tensor
+//    memory, O += P V with P read from tensor memory. Up to 64 columns P has columns of its own, so
+//    the next S runs while this one is in its softmax; above, P lies over S (two tiles' S and O fill
+//    tensor memory) and the other tile's work fills the wait.
+//  * warp 3: the guard. It waits for every V tile and, where the tile has masked elements, sets its
+//    infinities and NaN to zero: a zero probability times them would be NaN in rows that do not see
+//    them. (Rows that do see one add it in the epilogue.) With a bias it also copies the 383 values
+//    that the tile's distances can take into shared memory.
+//  * four warps per query tile: one row a thread, fp32 maximum and sum, exp2, P rounded to the
+//    input's type. The running maximum is raised only when it grows by more than 2^8.
+// Few query rows: the CTAs of a cluster take equal parts of the key tiles and join (m, l, O) through
+// distributed shared memory in rank order, so the result does not depend on timing and no workspace
+// is needed. Heads that share a key head are rows of the same tile then.
+//
+// All waits on mbarriers are bounded; see attn_common.cuh.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "attn_common.cuh"
+#include "sd_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace sd {
+namespace masked {
+
+using namespace sm100;
+using sd::attn::BM;
+using sd::attn::wait_bar;
+
+struct Params {
+  void* out;
+  const uint16_t* v;
+  const float* bias;  // [heads, 2 R + 1]
+  const int32_t *kv_lens, *q_starts, *prefix_lens, *q_offsets, *k_offsets;
+  long long o_batch, o_token, o_head;  // strides in elements
+  long long v_batch, v_token, v_head;
+  int heads, group;      // query heads; query heads per key head
+  int pack;              // heads that are rows of one tile (1 or group)
+  int Lq, Lk, dh, docs, radius, causal;
+  int tiles;             // CTAs (clusters) per (batch, packed head)
+  float scale_log2;      // scale * log2(e)
+  float cap_in, cap_out; // 2 log2(e) scale / cap, cap log2(e)
+  unsigned int* err;
+};
+
+// What a query sees: keys [lo, hi); distance of key j from query i: j - i + shift.
+struct Row {
+  int lo, hi;
+  long long shift;
+  bool exists;  // in the tensor, and in a document if there are any
+};
+
+constexpr long long kStartLimit = 1LL << 30;
+
+__device__ __forceinline__ long long clampll(long long v, long long lo, long long hi) {
+  return v < lo ? lo : v > hi ? hi : v;
+}
+
+__device__ inline Row row_of(const Params& p, int b, int i) {
+  Row r{0, 0, 0, false};
+  if (i >= p.Lq) return r;
+  long long q0 = 0, k0 = 0, nq = p.Lq, nk = p.Lk;
+  int s = b;
+  if (p.docs) {
+    int a = 0, e = p.docs + 1;  // number of offsets <= i
+    while (a < e) {
+      const int m = (a + e) >> 1;
+      if (p.q_offsets[m] <= i) a = m + 1;
+      else e = m;
+    }
+    s = a - 1;
+    if (s < 0 || s >= p.docs) {  // before the first or behind the last document
+      r.lo = r.hi = static_cast<int>(clampll(p.k_offsets[s < 0 ? 0 : p.docs], 0, p.Lk));
+      return r;
+    }
+    q0 = p.q_offsets[s];
+    nq = p.q_offsets[s + 1] - q0;
+    k0 = clampll(p.k_offsets[s], 0, p.Lk);
+    nk = clampll(p.k_offsets[s + 1], k0, p.Lk) - k0;
+  }
+  long long start = nk - nq;  // of the whole tensors without documents
+  if (p.q_starts) start = clampll(p.q_starts[s], -kStartLimit, kStartLimit);
+  if (p.kv_lens) nk = clampll(p.kv_lens[b], 0, p.Lk);
+  long long seen = nk;
+  if (p.causal) {
+    seen = start + (i - q0) + 1;
+    if (p.prefix_lens && p.prefix_lens[s] > seen) seen = p.prefix_lens[s];
+    seen = clampll(seen, 0, nk);
+  }
+  r.lo = static_cast<int>(k0);
+  r.hi = static_cast<int>(k0 + seen);
+  r.shift = q0 - k0 - start;
+  r.exists = true;
+  return r;
+}
+
+// DHT: padded head size (64-column chunks of shared memory; N of O is dh rounded up to 16).
+template <int DHT_, int BN_, int NQ_, int STAGES_, bool P_SEP_, bool F16_, bool CAP_, bool BIAS_>
+struct Cfg {
+  static constexpr int DHT = DHT_, BN = BN_, NQ = NQ_, STAGES = STAGES_;
+  static constexpr bool P_SEP = P_SEP_, F16 = F16_, CAP = CAP_, BIAS = BIAS_;
+  static constexpr int NCH = (DHT + 63) / 64;
+  static constexpr int Q_TILE = NCH * BM * 128, KV_TILE = NCH * BN * 128;
+  static constexpr int K_OFF = NQ * Q_TILE, V_OFF = K_OFF + STAGES * KV_TILE;
+  static constexpr int BIAS_OFF = V_OFF + STAGES * KV_TILE;
+  static constexpr int WINDOW = NQ * BM + BN;  // values of one bias window (one unused)
+  static constexpr int BAR_OFF = BIAS_OFF + (BIAS ? STAGES * WINDOW * 4 : 0);
+  // q_full, k_full[S], v_full[S], v_ready[S], kv_empty[S], bias_full[S], s_full, s_free, p_full, o_done, fin [NQ]
+  static constexpr int NBARS = 1 + 5 * STAGES + 5 * NQ;
+  static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // TMEM address, abort flag, cleaned flag, mixed flag
+  static constexpr int BOUNDS_OFF = MISC_OFF + 16;      // per query tile: lo of its first and last row, hi of both
+  static constexpr int SMEM = BOUNDS_OFF + NQ * 16 + 1024;
+  static constexpr int TM_P = P_SEP ? BN : 0, TM_O = P_SEP ? BN + BN / 2 : BN;
+  static constexpr int TM_TILE = TM_O + DHT <= 256 ? 256 : 512;
+  static constexpr int TM_COLS = NQ * TM_TILE;
+  static constexpr int THREADS = 128 + 128 * NQ;
+  static constexpr int REG_HELPER = 120, REG_SOFT = 192;
+  // Of every 8 column pairs this many take exp2 on the FMA pipe; with a cap or bias that pipe has other work.
+  static constexpr int POLY = CAP || BIAS ? 0 : 2;
+  // Join of a cluster's parts: rows of DHT fp32 and (m, l), over the K/V ring.
+  static constexpr int JOIN_ROW = DHT + 4;  // floats a row (+4: rows start in different banks)
+  static_assert(TM_COLS <= 512 && SMEM <= 227 * 1024, "on-chip memory");
+  static_assert(NQ != 1 || BM * JOIN_ROW * 4 <= 2 * STAGES * KV_TILE, "the join fits the ring");
+  static_assert(NQ != 2 || 128 * REG_HELPER + 256 * REG_SOFT <= 168 * 384, "register split");
+};
+
+struct Bars {
+  uint32_t base;
+  int S, nq;
+  __device__ uint32_t q_full() const { return base; }
+  __device__ uint32_t k_full(int s) const { return base + 8 * (1 + s); }
+  __device__ uint32_t v_full(int s) const { return base + 8 * (1 + S + s); }
+  __device__ uint32_t v_ready(int s) const { return base + 8 * (1 + 2 * S + s); }
+  __device__ uint32_t kv_empty(int s) const { return base + 8 * (1 + 3 * S + s); }
+  __device__ uint32_t bias_full(int s) const { return base + 8 * (1 + 4 * S + s); }
+  __device__ uint32_t s_full(int t) const { return base + 8 * (1 + 5 * S + t); }
+  __device__ uint32_t s_free(int t) const { return base + 8 * (1 + 5 * S + nq + t); }
+  __device__ uint32_t p_full(int t) const { return base + 8 * (1 + 5 * S + 2 * nq + t); }
+  __device__ uint32_t o_done(int t) const { return base + 8 * (1 + 5 * S + 3 * nq + t); }
+  __device__ uint32_t fin(int t) const { return base + 8 * (1 + 5 * S + 4 * nq + t); }
+};
+
+// The key tiles of one query tile (or of all): [first, last), and which of them need masks.
+struct Bounds {
+  int lo_first, lo_last, hi_first, hi_last;
+  __device__ bool empty() const { return hi_last <= lo_first; }
+  template <int BN>
+  __device__ int first() const { return lo_first / BN; }
+  template <int BN>
+  __device__ int last() const { return (hi_last + BN - 1) / BN; }
+  template <int BN>
+  __device__ bool holds(int j) const { return !empty() && j >= first<BN>() && j < last<BN>(); }
+  template <int BN>
+  __device__ bool whole(int j) const { return j * BN >= lo_last && (j + 1) * BN <= hi_first; }
+};
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// exp2_poly2 with an exact zero below 2^-125: a masked key's probability must not be merely small.
+__device__ __forceinline__ void exp2_poly2_zero(float& y0, float& y1, float x0, float x1) {
+  float a, b;
+  exp2_poly2(a, b, x0, x1);
+  y0 = x0 < -125.0f ? 0.f : a;
+  y1 = x1 < -125.0f ? 0.f : b;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float4 peer_load4(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    attention_masked_sm100(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
+  constexpr int BN = C::BN, NQ = C::NQ, STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const Bars bars{sbase + C::BAR_OFF, STAGES, NQ};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
+  volatile int* cleaned = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);  // the guard set a value to zero
+  volatile int* mixed = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 12);   // rows with different shifts
+  Bounds* bounds = reinterpret_cast<Bounds*>(smem + C::BOUNDS_OFF);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int splits = NQ == 1 ? static_cast<int>(cluster_size()) : 1;
+  const int rank = NQ == 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int item = blockIdx.x / splits;
+  // Late queries first: with a causal mask they see the most keys.
+  const int qt = p.tiles - 1 - item % p.tiles;
+  const int heads_packed = p.heads / p.pack;
+  const int bh = item / p.tiles, b = bh / heads_packed, h0 = bh % heads_packed * p.pack, kvh = h0 / p.group;
+  const long long rows = static_cast<long long>(p.Lq) * p.pack;    // of this (batch, packed head)
+  const long long row0 = static_cast<long long>(qt) * (NQ * BM);
+
+  if (threadIdx.x == 0) {
+    mbar_init(bars.q_full(), 1);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(bars.k_full(s), 1);
+      mbar_init(bars.v_full(s), 1);
+      mbar_init(bars.v_ready(s), 1);
+      mbar_init(bars.kv_empty(s), NQ);
+      mbar_init(bars.bias_full(s), 1);
+    }
+    for (int t = 0; t < NQ; ++t) {
+      mbar_init(bars.s_full(t), 1);
+      mbar_init(bars.s_free(t), 128);
+      mbar_init(bars.p_full(t), 128);
+      mbar_init(bars.o_done(t), 1);
+      mbar_init(bars.fin(t), 1);
+    }
+    *abort_flag = 0;
+    *cleaned = 0;
+    *mixed = 0;
+    for (int t = 0; t < NQ; ++t) bounds[t] = Bounds{0, 0, 0, 0};
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), C::TM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  sd::grid_dep_wait();  // global memory from here on
+  sd::grid_dep_launch();
+
+  Row me{0, 0, 0, false};
+  const int r_in = static_cast<int>(threadIdx.x) - 128;  // row within the CTA (softmax threads)
+  if (r_in >= 0) {
+    const long long r = row0 + r_in;
+    if (r < rows) {
+      me = row_of(p, b, static_cast<int>(r / p.pack));
+      const int t = r_in / BM;
+      if (r_in % BM == 0) bounds[t].lo_first = me.lo, bounds[t].hi_first = me.hi;
+      if (r_in % BM == BM - 1 || r == rows - 1) bounds[t].lo_last = me.lo, bounds[t].hi_last = me.hi;
+    }
+  }
+  __syncthreads();
+  long long shift0 = 0;
+  if constexpr (C::BIAS) {
+    // The window of distances assumes one shift for the CTA's rows; documents may differ in theirs.
+    shift0 = row_of(p, b, static_cast<int>(row0 / p.pack)).shift;
+    if (me.exists && me.hi > me.lo && me.shift != shift0) *mixed = 1;
+    __syncthreads();
+  }
+  Bounds tb[NQ];
+#pragma unroll
+  for (int t = 0; t < NQ; ++t) tb[t] = bounds[t];
+  int j0 = 0x7fffffff, j1 = 0;
+#pragma unroll
+  for (int t = 0; t < NQ; ++t)
+    if (!tb[t].empty()) j0 = min(j0, tb[t].template first<BN>()), j1 = max(j1, tb[t].template last<BN>());
+  if (j1 <= j0) j0 = j1 = 0;
+  if (NQ == 1 && splits > 1) {  // this CTA's part of the key tiles
+    const long long n = j1 - j0;
+    const int a = j0 + static_cast<int>(n * rank / splits), e = j0 + static_cast<int>(n * (rank + 1) / splits);
+    j0 = a, j1 = e;
+  }
+
+  if (warp < 4) {
+    // ================================================================== helper warpgroup
+    if constexpr (NQ == 2) regs_dec<C::REG_HELPER>();
+    const int chunks = (p.dh + 63) / 64;
+    if (warp == 0) {
+      // ---------------------------------------------------------------- TMA producer
+      if (lane == 0 && j1 > j0) {
+        mbar_arrive_expect_tx(bars.q_full(), NQ * chunks * BM * 128);
+        for (int t = 0; t < NQ; ++t)
+          for (int c = 0; c < chunks; ++c)
+            tma_load_4d(sbase + t * C::Q_TILE + c * BM * 128, &tm_q, bars.q_full(), c * 64, h0,
+                        static_cast<int>((row0 + t * BM) / p.pack), b);
+        int g = 0;
+        for (int j = j0; j < j1; ++j, ++g) {
+          const int s = g % STAGES;
+          if (g >= STAGES && !wait_bar(bars.kv_empty(s), (g / STAGES - 1) & 1, abort_flag, p.err)) break;
+          mbar_arrive_expect_tx(bars.k_full(s), chunks * BN * 128);
+          for (int c = 0; c < chunks; ++c)
+            tma_load_4d(sbase + C::K_OFF + s * C::KV_TILE + c * BN * 128, &tm_k, bars.k_full(s), c * 64, kvh, j * BN, b);
+          mbar_arrive_expect_tx(bars.v_full(s), chunks * BN * 128);
+          for (int c = 0; c < chunks; ++c)
+            tma_load_4d(sbase + C::V_OFF + s * C::KV_TILE + c * BN * 128, &tm_v, bars.v_full(s), c * 64, kvh, j * BN, b);
+        }
+        // Every copy has landed before the CTA may exit.
+        wait_bar(bars.q_full(), 0, abort_flag, p.err, false);
+        for (int k = max(0, g - STAGES); k < g; ++k) {
+          wait_bar(bars.k_full(k % STAGES), (k / STAGES) & 1, abort_flag, p.err, false);
+          wait_bar(bars.v_full(k % STAGES), (k / STAGES) & 1, abort_flag, p.err, false);
+        }
+      }
+      __syncwarp();
+    } else if (warp <= NQ) {
+      // ---------------------------------------------------------------- MMA issuer of query tile t
+      const int t = warp - 1;
+      if (lane == 0) {
+        const int ksteps = (p.dh + 15) / 16;
+        constexpr uint32_t idesc_qk = idesc_f16kind_f32(BM, BN, false, C::F16);
+        const uint32_t idesc_pv = idesc_f16kind_f32(BM, 16, true, C::F16) + (static_cast<uint32_t>((ksteps * 16 - 16) >> 3) << 17);
+        const uint32_t tS = tmem + t * C::TM_TILE, tP = tS + C::TM_P, tO = tS + C::TM_O;
+        const uint32_t tq = sbase + t * C::Q_TILE;
+        auto issue_qk = [&](int s) {
+          for (int ks = 0; ks < ksteps; ++ks) {
+            const uint64_t a = smem_desc(tq + (ks >> 2) * (BM * 128) + (ks & 3) * 32, 16, 1024);
+            const uint64_t bd = smem_desc(sbase + C::K_OFF + s * C::KV_TILE + (ks >> 2) * (BN * 128) + (ks & 3) * 32, 16, 1024);
+            mma_ss(tS, a, bd, idesc_qk, ks > 0 ? 1u : 0u);
+          }
+          mma_commit(bars.s_full(t));
+        };
+        auto issue_pv = [&](int s, bool first) {
+#pragma unroll
+          for (int ks = 0; ks < BN / 16; ++ks) {
+            const uint64_t bd = smem_desc(sbase + C::V_OFF + s * C::KV_TILE + ks * 16 * 128, BN * 128, 1024);
+            mma_ts(tO, tP + ks * 8, bd, idesc_pv, (!first || ks > 0) ? 1u : 0u);
+          }
+          mma_commit(bars.o_done(t));
+          mma_commit(bars.kv_empty(s));
+        };
+        // S of the next tile is issued before P V of this one, as soon as S has been read; where P lies
+        // over S, once P V is complete. Key tiles that this query tile does not need are released as
+        // they arrive, after the P V that is still to come: its own stage must not wait for them.
+        bool ok = j1 <= j0 || wait_bar(bars.q_full(), 0, abort_flag, p.err);
+        int n = 0, pending = -1;  // S issued so far; ring position of the tile whose P V is still to come
+        auto finish = [&] {
+          if (pending < 0) return true;
+          if (!wait_bar(bars.p_full(t), (n - 1) & 1, abort_flag, p.err)) return false;
+          if (!wait_bar(bars.v_ready(pending % STAGES), (pending / STAGES) & 1, abort_flag, p.err)) return false;
+          tc_fence_after();
+          issue_pv(pending % STAGES, n == 1);
+          pending = -1;
+          return true;
+        };
+        for (int j = j0, g = 0; ok && j < j1; ++j, ++g) {
+          const int s = g % STAGES;
+          const bool held = tb[t].template holds<BN>(j);
+          if ((!held || !C::P_SEP) && !(ok = finish())) break;
+          if (!(ok = wait_bar(bars.k_full(s), (g / STAGES) & 1, abort_flag, p.err))) break;
+          if (!held) {
+            mbar_arrive(bars.kv_empty(s));
+            continue;
+          }
+          if (n > 0 && !(ok = wait_bar(C::P_SEP ? bars.s_free(t) : bars.o_done(t), (n - 1) & 1, abort_flag, p.err))) break;
+          tc_fence_after();
+          issue_qk(s);
+          // (P_SEP) the counts of finish() are those before this S
+          if (C::P_SEP && !(ok = finish())) break;
+          ++n;
+          pending = g;
+        }
+        if (ok) finish();
+        mma_commit(bars.fin(t));
+        wait_bar(bars.fin(t), 0, abort_flag, p.err, false);
+      }
+      __syncwarp();
+    } else if (warp == 3) {
+      // ---------------------------------------------------------------- guard
+      int g = 0;
+      for (int j = j0; j < j1; ++j, ++g) {
+        const int s = g % STAGES;
+        if constexpr (C::BIAS) {
+          if (g >= STAGES && !__all_sync(0xffffffffu, wait_bar(bars.kv_empty(s), (g / STAGES - 1) & 1, abort_flag, p.err))) break;
+          // Window value e belongs to the distance d0 + e.
+          const long long d0 = static_cast<long long>(j) * BN - (row0 / p.pack + NQ * BM - 1) + shift0;
+          const float* table = p.bias + static_cast<long long>(h0) * (2LL * p.radius + 1) + p.radius;
+          float* w = reinterpret_cast<float*>(smem + C::BIAS_OFF) + s * C::WINDOW;
+#pragma unroll
+          for (int i = 0; i < C::WINDOW / 32; ++i) {
+            const float x = __ldg(table + clampll(d0 + i * 32 + lane, -p.radius, p.radius));
+            const float y = x * 1.4426950408889634f;
+            // the lowest finite value stays finite in units of log2
+            w[i * 32 + lane] = isinf(y) && !isinf(x) ? copysignf(3.402823466e38f, x) : y;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars.bias_full(s));
+        }
+        if (!__all_sync(0xffffffffu, wait_bar(bars.v_full(s), (g / STAGES) & 1, abort_flag, p.err))) break;
+        bool masks = false;
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) masks |= tb[t].template holds<BN>(j) && !tb[t].template whole<BN>(j);
+        if (masks) {
+          uint4* tile = reinterpret_cast<uint4*>(smem + C::V_OFF + s * C::KV_TILE);
+          const int n = chunks * BN * 8;
+          constexpr uint32_t kExp = C::F16 ? 0x7c00u : 0x7f80u;  // all exponent bits set: infinity or NaN
+          bool found = false;
+          for (int i = lane; i < n; i += 32) {
+            uint4 x = tile[i];
+            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if ((w[k] & kExp) == kExp) w[k] &= 0xffff0000u, bad = true;
+              if ((w[k] >> 16 & kExp) == kExp) w[k] &= 0xffffu, bad = true;
+            }
+            if (bad) tile[i] = x, found = true;
+          }
+          if (__any_sync(0xffffffffu, found)) {
+            if (lane == 0) *cleaned = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
+        if (lane == 0) mbar_arrive(bars.v_ready(s));
+      }
+    }
+  } else {
+    // ================================================================== softmax warpgroups
+    if constexpr (NQ == 2) regs_inc<C::REG_SOFT>();
+    const int t = r_in / BM, quarter = warp & 3;
+    const uint32_t tbase = tmem + t * C::TM_TILE + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t tS = tbase, tP = tbase + C::TM_P, tO = tbase + C::TM_O;
+    Bounds mine = tb[0];
+    if (NQ == 2 && t == 1) mine = tb[NQ - 1];
+    const long long row = row0 + r_in;
+    const bool live = row0 + (r_in & ~31) < rows;  // a warp behind the last row only keeps the barriers going
+    const bool is_mixed = C::BIAS && *mixed;
+    const int ochunks = (p.dh + 15) / 16;
+    float m_run = -INFINITY, l_run = 0.f;
+    bool ok = true;
+    int n = 0;
+    for (int j = j0, g = 0; j < j1; ++j, ++g) {
+      if (!mine.template holds<BN>(j)) continue;
+      if (!__all_sync(0xffffffffu, wait_bar(bars.s_full(t), n & 1, abort_flag, p.err))) {
+        ok = false;
+        break;
+      }
+      if (C::BIAS && !__all_sync(0xffffffffu, wait_bar(bars.bias_full(g % STAGES), (g / STAGES) & 1, abort_flag, p.err))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      if (!live) {
+        tc_fence_before();
+        if (C::P_SEP) mbar_arrive(bars.s_free(t));
+        // as the other warps: no arrival for this P before every warp's for the one before it
+        if (n > 0 && !__all_sync(0xffffffffu, wait_bar(bars.o_done(t), (n - 1) & 1, abort_flag, p.err))) {
+          ok = false;
+          break;
+        }
+        mbar_arrive(bars.p_full(t));
+        ++n;
+        continue;
+      }
+      float sv[BN];
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) {
+        uint32_t r[32];
+        tmem_ld32(tS + c * 32, r);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(r[i]);
+      }
+      tmem_wait_ld();
+      if constexpr (C::P_SEP) {
+        tc_fence_before();
+        mbar_arrive(bars.s_free(t));
+      }
+      if constexpr (C::CAP) {
+        // cap log2(e) tanh(x / cap) = cap log2(e) (1 - 2 / (1 + exp(2 x / cap)))
+#pragma unroll
+        for (int i = 0; i < BN; ++i)
+          sv[i] = fmaf(-2.f * p.cap_out, rcp_approx(1.f + ex2_approx(sv[i] * p.cap_in)), p.cap_out);
+      }
+      if constexpr (C::BIAS) {
+        if (!is_mixed) {
+          const float* w = reinterpret_cast<const float*>(smem + C::BIAS_OFF) + (g % STAGES) * C::WINDOW + (NQ * BM - 1 - r_in);
+#pragma unroll
+          for (int i = 0; i < BN; ++i) sv[i] = C::CAP ? sv[i] + w[i] : fmaf(sv[i], p.scale_log2, w[i]);
+        } else {  // a tile over documents with different shifts: each row its own distances
+          const float* table = p.bias + static_cast<long long>(h0) * (2LL * p.radius + 1) + p.radius;
+          const long long d0 = static_cast<long long>(j) * BN - row / p.pack + me.shift;
+#pragma unroll
+          for (int i = 0; i < BN; ++i) {
+            const float x = __ldg(table + clampll(d0 + i, -p.radius, p.radius));
+            float y = x * 1.4426950408889634f;
+            if (isinf(y) && !isinf(x)) y = copysignf(3.402823466e38f, x);
+            sv[i] = C::CAP ? sv[i] + y : fmaf(sv[i], p.scale_log2, y);
+          }
+        }
+      }
+      if (!mine.template whole<BN>(j)) {
+        const int lo = me.lo - j * BN, hi = me.hi - j * BN;
+#pragma unroll
+        for (int i = 0; i < BN; ++i)
+          if (i < lo || i >= hi) sv[i] = -INFINITY;
+      }
+      float pm[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) pm[k] = sv[k];
+#pragma unroll
+      for (int i = 8; i + 16 <= BN; i += 16)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) pm[k] = max3f(pm[k], sv[i + k], sv[i + 8 + k]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], sv[BN - 8 + k]);
+      const float mx = max3f(max3f(pm[0], pm[1], pm[2]), max3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+      constexpr bool kLog2 = C::CAP || C::BIAS;  // sv is in units of log2 already
+      const float m_new = fmaxf(m_run, kLog2 ? mx : mx * p.scale_log2);
+      // Row by row: no row's bits depend on its neighbours' scores.
+      const bool raise = m_new > m_run + 8.0f, rescale = __any_sync(0xffffffffu, raise);
+      const float alpha = !raise ? 1.0f : m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
+      if (raise) m_run = m_new;
+      const float neg_m = m_run == -INFINITY ? 0.f : -m_run;  // a row that has seen nothing: all its exp2 are 0
+      uint32_t pk[BN / 2];
+      float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
+#pragma unroll
+      for (int i = 0; i < BN / 2; ++i) {
+        float x0, x1;
+        if constexpr (kLog2) add2(x0, x1, sv[2 * i], sv[2 * i + 1], neg_m, neg_m);
+        else fma2(x0, x1, sv[2 * i], sv[2 * i + 1], p.scale_log2, p.scale_log2, neg_m, neg_m);
+        if ((i & 7) < C::POLY) {
+          exp2_poly2_zero(x0, x1, x0, x1);
+        } else {
+          x0 = ex2_approx(x0);
+          x1 = ex2_approx(x1);
+        }
+        if (i & 1) add2(ls2, ls3, ls2, ls3, x0, x1);
+        else add2(ls0, ls1, ls0, ls1, x0, x1);
+        pk[i] = C::F16 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
+      }
+      l_run = fmaf(l_run, alpha, (ls0 + ls1) + (ls2 + ls3));
+      if (n > 0) {
+        if (!__all_sync(0xffffffffu, wait_bar(bars.o_done(t), (n - 1) & 1, abort_flag, p.err))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (rescale) {
+          for (int c = 0; c < ochunks; ++c) {
+            uint32_t r[16];
+            tmem_ld16(tO + c * 16, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
+            tmem_st16(tO + c * 16, r);
+          }
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < BN / 32; ++c) {
+        uint32_t r[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = pk[c * 16 + i];
+        tmem_st16(tP + c * 16, r);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bars.p_full(t));
+      ++n;
+    }
+    if (ok && n > 0) ok = __all_sync(0xffffffffu, wait_bar(bars.o_done(t), (n - 1) & 1, abort_flag, p.err));
+    tc_fence_after();
+    // ------------------------------------------------------------------ epilogue, one row a thread
+    const int i_q = static_cast<int>(row / p.pack), h = h0 + static_cast<int>(row % p.pack);
+    // Values that the guard set to zero, for rows that see them: 16 columns from c16 of the masked tiles.
+    auto add_cleaned = [&](int c16, float (&o)[16]) {
+      const uint16_t* v = p.v + b * p.v_batch + kvh * p.v_head + c16;
+      for (int j = j0; j < j1; ++j) {
+        bool masks = false;
+#pragma unroll
+        for (int u = 0; u < NQ; ++u) masks |= tb[u].template holds<BN>(j) && !tb[u].template whole<BN>(j);
+        if (!masks) continue;
+        for (int key = max(me.lo, j * BN); key < min(me.hi, (j + 1) * BN); ++key) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (c16 + i >= p.dh) continue;
+            const uint32_t w = v[key * p.v_token + i];
+            if (C::F16 ? (w & 0x7c00u) == 0x7c00u : (w & 0x7f80u) == 0x7f80u) {
+              const bool nan = C::F16 ? (w & 0x3ffu) != 0 : (w & 0x7fu) != 0;
+              o[i] += __uint_as_float(nan ? 0x7fc00000u : 0x7f800000u | (w & 0x8000u) << 16);
+            }
+          }
+        }
+      }
+    };
+    const bool has_o = n > 0 && ok, fix = has_o && *cleaned;  // the same for the warp
+    const bool join = NQ == 1 && splits > 1;
+    const bool store = row < rows && (join || (me.exists && ok));
+    // A part of a cluster's join goes over the ring: its copies and MMAs are done with the last P V.
+    float* part = reinterpret_cast<float*>(smem + C::K_OFF) + (NQ == 1 ? r_in : 0) * C::JOIN_ROW;
+    uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.o_batch + i_q * p.o_token + h * p.o_head;
+    const float inv = join ? 1.f : l_run == 0.f ? 0.f : 1.0f / l_run;
+    if (live) {
+      for (int c = 0; c < ochunks; ++c) {
+        float o[16];
+        if (has_o) {  // warp-wide: every lane takes part
+          uint32_t r[16];
+          __syncwarp();
+          tmem_ld16(tO + c * 16, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = l_run == 0.f ? 0.f : __uint_as_float(r[i]) * inv;
+          if (fix && store) add_cleaned(c * 16, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = 0.f;
+        }
+        if (!store) continue;
+        if (join) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<float4*>(part + c * 16)[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else {
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = C::F16 ? pack_f16x2(o[2 * i], o[2 * i + 1]) : pack_bf16x2(o[2 * i], o[2 * i + 1]);
+          uint4* dst = reinterpret_cast<uint4*>(out + c * 16);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          if (c * 16 + 8 < p.dh) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+      if (join && store) {
+        part[C::DHT] = m_run;
+        part[C::DHT + 1] = l_run;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TM_COLS);
+  }
+  if constexpr (NQ == 1) {
+    if (splits > 1) {
+      // Join: the rows are dealt to the CTAs; each output value is summed over the parts in rank order.
+      cluster_sync();
+      const int live_rows = static_cast<int>(min(rows - row0, static_cast<long long>(BM)));
+      const int groups = p.dh / 8;  // 8 columns a thread
+      const uint32_t base = sbase + C::K_OFF;
+      if (!*abort_flag)
+        for (int w = rank * C::THREADS + static_cast<int>(threadIdx.x); w < live_rows * groups; w += splits * C::THREADS) {
+          const int r = w / groups, c = w % groups * 8;
+          const Row info = row_of(p, b, static_cast<int>((row0 + r) / p.pack));
+          float m = -INFINITY;
+          for (int k = 0; k < splits; ++k) m = fmaxf(m, peer_load4(base + (r * C::JOIN_ROW + C::DHT) * 4, k).x);
+          float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          for (int k = 0; k < splits; ++k) {
+            const float4 ml = peer_load4(base + (r * C::JOIN_ROW + C::DHT) * 4, k);
+            if (ml.y == 0.f) continue;  // this part has no key that the row sees
+            const float a = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
+            const float4 x = peer_load4(base + (r * C::JOIN_ROW + c) * 4, k);
+            const float4 y = peer_load4(base + (r * C::JOIN_ROW + c + 4) * 4, k);
+            l = fmaf(ml.y, a, l);
+            o[0] = fmaf(x.x, a, o[0]), o[1] = fmaf(x.y, a, o[1]), o[2] = fmaf(x.z, a, o[2]), o[3] = fmaf(x.w, a, o[3]);
+            o[4] = fmaf(y.x, a, o[4]), o[5] = fmaf(y.y, a, o[5]), o[6] = fmaf(y.z, a, o[6]), o[7] = fmaf(y.w, a, o[7]);
+          }
+          if (!info.exists) continue;
+          const float inv = l == 0.f ? 0.f : 1.0f / l;
+          uint32_t q[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            q[i] = C::F16 ? pack_f16x2(o[2 * i] * inv, o[2 * i + 1] * inv) : pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+          const long long at = row0 + r;
+          uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.o_batch + (at / p.pack) * p.o_token + (h0 + at % p.pack) * p.o_head;
+          *reinterpret_cast<uint4*>(out + c) = make_uint4(q[0], q[1], q[2], q[3]);
+        }
+      cluster_sync();  // no CTA leaves while a peer reads its part
+    }
+  }
+}
+
+}  // namespace masked
+}  // namespace sd

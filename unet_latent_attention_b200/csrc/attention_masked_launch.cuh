@@ -1,0 +1,109 @@
+// Launch of one attention_masked_sm100 configuration and the choice among those of a head size.
+#pragma once
+
+#include <algorithm>
+#include <atomic>
+
+#include "attention_masked.cuh"
+#include "attention_masked.h"
+
+namespace sd {
+namespace masked {
+
+constexpr int kMaxSplits = 8;  // CTAs of a portable cluster
+
+template <class C>
+sd_status launch(const Launch& l, int pack, int64_t tiles, int splits) {
+  const sd_attention_masked_args& a = *l.args;
+  const int64_t keys = std::max<int64_t>(a.Lk, 1);  // a tensor map has no empty dimension; without keys nothing is loaded
+  CUtensorMap mq, mk, mv;
+  sd_status st = make_view_map(&mq, a.q, a.q_stride, a.B, a.Lq, a.heads, a.dh, pack, BM / pack, C::F16);
+  if (st == SD_OK) st = make_view_map(&mk, a.k, a.k_stride, a.B, keys, a.kv_heads, a.dh, 1, C::BN, C::F16);
+  if (st == SD_OK) st = make_view_map(&mv, a.v, a.v_stride, a.B, keys, a.kv_heads, a.dh, 1, C::BN, C::F16);
+  if (st != SD_OK) return st;
+  Params p = {};
+  p.out = a.o;
+  p.v = static_cast<const uint16_t*>(a.v);
+  p.bias = a.bias;
+  p.kv_lens = a.kv_lens, p.q_starts = a.q_starts, p.prefix_lens = a.prefix_lens;
+  p.q_offsets = a.q_offsets, p.k_offsets = a.k_offsets;
+  p.o_batch = a.o_stride[0], p.o_token = a.o_stride[1], p.o_head = a.o_stride[2];
+  p.v_batch = a.v_stride[0], p.v_token = a.v_stride[1], p.v_head = a.v_stride[2];
+  p.heads = static_cast<int>(a.heads), p.group = static_cast<int>(l.group), p.pack = pack;
+  p.Lq = static_cast<int>(a.Lq), p.Lk = static_cast<int>(a.Lk), p.dh = static_cast<int>(a.dh);
+  p.docs = a.q_offsets ? static_cast<int>(a.docs) : 0;
+  p.radius = static_cast<int>(a.bias_radius), p.causal = a.causal;
+  p.tiles = static_cast<int>(tiles);
+  constexpr float kLog2e = 1.4426950408889634f;
+  p.scale_log2 = std::max(a.scale * kLog2e, 1.17549435e-38f);  // scale 0: a masked score must not become 0 * -infinity
+  p.cap_in = C::CAP ? 2.f * kLog2e * (a.scale / a.cap) : 0.f;
+  p.cap_out = a.cap * kLog2e;
+  p.err = sd::device_status_word();
+  if (!p.err) return SD_ERR_CUDA;
+
+  auto kern = attention_masked_sm100<C>;
+  static std::atomic<uint64_t> smem_set{0};  // one bit per device: opt-in to large shared memory done
+  int dev = 0;
+  st = sd::cuda_check(cudaGetDevice(&dev), "cudaGetDevice");
+  if (st != SD_OK) return st;
+  const uint64_t bit = uint64_t(1) << (dev & 63);
+  if (!(smem_set.load(std::memory_order_acquire) & bit)) {
+    st = sd::cuda_check(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM),
+                        "cudaFuncSetAttribute(attention_masked smem)");
+    if (st != SD_OK) return st;
+    smem_set.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const int64_t ctas = a.B * (a.heads / pack) * tiles * splits;
+  if (ctas > 0x7fffffff) return sd::fail(SD_ERR_UNSUPPORTED, "sd_attention_masked: too many query tiles");
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = l.stream;
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  cfg.numAttrs = sd::pdl_attr(&attr[0]);
+  if (splits > 1) {
+    attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    attr[cfg.numAttrs].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  return sd::cuda_check(cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p), "sd_attention_masked launch");
+}
+
+// Two = the configuration of two query tiles a CTA (one where tensor memory holds no more), One = of one.
+template <class Two, class One>
+sd_status choose(const Launch& l) {
+  const sd_attention_masked_args& a = *l.args;
+  // Heads that share a key head become rows of one tile while that fills tiles better: few queries.
+  // (The bias of a row's head would differ within a tile.)
+  int pack = 1;
+  if (!One::BIAS && a.Lq <= BM / 2 && l.group > 1 && BM % l.group == 0) pack = static_cast<int>(l.group);
+  const int64_t planes = a.B * (a.heads / pack), rows = a.Lq * pack;
+  const int64_t one = (rows + BM - 1) / BM, two = (rows + 2 * BM - 1) / (2 * BM);
+  // One tile a CTA while each can have an SM of its own.
+  if (Two::NQ == 1 || planes * one <= sd::sm_count()) {
+    // Idle SMs: split the keys over a cluster, two key tiles a CTA at least.
+    int splits = 1;
+    const int64_t key_tiles = (a.Lk + One::BN - 1) / One::BN;
+    while (2 * splits <= kMaxSplits && planes * one * 2 * splits <= sd::sm_count() && key_tiles >= 4 * splits) splits *= 2;
+    return launch<One>(l, pack, one, splits);
+  }
+  return launch<Two>(l, pack, two, 1);
+}
+
+template <int DHT, int BN, int NQ2, int STAGES2, int STAGES1, bool P_SEP2, bool P_SEP1, bool F16>
+sd_status by_score(const Launch& l) {
+  const bool cap = l.args->cap != 0.f, bias = l.args->bias != nullptr;
+  if (cap && bias)
+    return choose<Cfg<DHT, BN, NQ2, STAGES2, P_SEP2, F16, true, true>, Cfg<DHT, BN, 1, STAGES1, P_SEP1, F16, true, true>>(l);
+  if (cap)
+    return choose<Cfg<DHT, BN, NQ2, STAGES2, P_SEP2, F16, true, false>, Cfg<DHT, BN, 1, STAGES1, P_SEP1, F16, true, false>>(l);
+  if (bias)
+    return choose<Cfg<DHT, BN, NQ2, STAGES2, P_SEP2, F16, false, true>, Cfg<DHT, BN, 1, STAGES1, P_SEP1, F16, false, true>>(l);
+  return choose<Cfg<DHT, BN, NQ2, STAGES2, P_SEP2, F16, false, false>, Cfg<DHT, BN, 1, STAGES1, P_SEP1, F16, false, false>>(l);
+}
+
+}  // namespace masked
+}  // namespace sd

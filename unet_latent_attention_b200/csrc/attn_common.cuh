@@ -4,6 +4,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -46,6 +47,9 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, 
   else sm100::tma_load_3d(dst, map, bar, x, row, bh);
 }
 #endif
+
+// cuTensorMapEncodeTiled of the driver, or nullptr.
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 
 // Tensor map over a contiguous 16-bit [planes, rows, dh] tensor with box {64, box_rows, 1} and
 // 128-byte swizzle (lay_heads = 0), or over [planes / heads, rows, heads, dh] as the 4-D map
