@@ -7,10 +7,12 @@
 //
 // Bound by HBM: every value is read once and written once, four operations each. So a row stays in
 // registers between the statistics and the output: a pack of 16 bytes per load, up to NV packs per
-// thread, all loads of a row in flight before the first is used. Many rows: one warp per row, whose
-// reductions are shuffles and which meets no barrier. Few rows (a decoding step) or wide ones: one
-// CTA per row, whose warps exchange one partial sum each through shared memory. Rows beyond what
-// 512 threads hold (kMaxThreads * kMaxPacks packs) are read twice (three times for one scale a row).
+// thread, all loads of a row in flight before the first is used. Narrow rows: one warp per row, whose
+// reductions are shuffles and which meets no barrier. Others: one CTA per row, whose warps exchange
+// one partial sum each through shared memory. Rows beyond what 512 threads hold (kMaxThreads *
+// kMaxPacks packs) are read twice. B200: [32760, 2048] bf16 with residual 80.6 us, 6650 GB/s (a plain
+// copy: 6560); [8192, 1280] into e4m3 with blocks of 128 15.8 us, 4670 GB/s, where the instructions of
+// the conversion share the time.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -28,7 +30,7 @@ constexpr float kE4m3Max = 448.0f;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: the scale of a block of zeros
 constexpr int kMaxThreads = 512;              // 128 registers a thread: a row's packs stay in them
 constexpr int kMaxPacks = 8;
-constexpr int kWarpRowThreads = 256;          // threads of a CTA that takes one row per warp
+constexpr int kWarpRows = 8;                  // rows of a CTA that takes one row per warp
 
 struct RmsArgs {
   const void* x;
@@ -39,8 +41,10 @@ struct RmsArgs {
   float* scales;         // e4m3: [rows, ceil(cols / block)], or [rows] for block = 0
   long long x_stride, residual_stride, y_stride, residual_out_stride;  // elements between rows
   long long rows;
-  int cols, block;
-  float eps;
+  int cols;
+  int block;        // columns with one scale: 32, 64 or 128, or 0: the row
+  int block_log2, nblocks;
+  float eps, inv_cols;
   int weight_f32;
 };
 
@@ -56,24 +60,38 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+// Over groups of `lanes` neighbouring lanes (a power of two, the same for the whole grid).
 __device__ __forceinline__ float lanes_max(float v, int lanes) {
-  for (int o = lanes >> 1; o; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    if (o < lanes) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
-// The row's sum or maximum over all threads that share it: the warp, or the CTA's warps through `part`.
-// Barriers bracket the use of `part`, so that two reductions of a row can follow one another.
-template <bool MAX>
-__device__ __forceinline__ float row_reduce(float v, bool warp_row, float* part) {
-  v = MAX ? lanes_max(v, 32) : warp_sum(v);
-  if (warp_row) return v;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  if (lane == 0) part[warp] = v;
+// The row's sum of squares and, where it has one scale, its largest magnitude, over all threads that
+// share it: the warp, or the CTA's warps with one exchange through shared memory (and one barrier: the
+// exchange is used once).
+struct Totals {
+  float sum, top;
+};
+template <bool TOP>
+__device__ __forceinline__ Totals row_totals(float sum, float top, bool warp_row, float (&part)[2][kMaxThreads / 32]) {
+  sum = warp_sum(sum);
+  if (TOP) top = lanes_max(top, 32);
+  if (warp_row) return {sum, top};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) {
+    part[0][warp] = sum;
+    if (TOP) part[1][warp] = top;
+  }
   __syncthreads();
-  v = lane < warps ? part[lane] : 0.f;  // the maxima are of magnitudes: 0 is their neutral element too
-  v = MAX ? lanes_max(v, 32) : warp_sum(v);
-  __syncthreads();
-  return v;
+  sum = part[0][0];
+  if (TOP) top = part[1][0];
+  for (int w = 1; w < static_cast<int>(blockDim.x >> 5); ++w) {  // every thread in the same order: broadcasts
+    sum += part[0][w];
+    if (TOP) top = max_nan(top, part[1][w]);
+  }
+  return {sum, top};
 }
 
 // Column of element e of pack p. VECT: packs are contiguous (one 16-byte access). Otherwise the 32
@@ -113,53 +131,51 @@ __device__ __forceinline__ void store_pack(T* row, int p, int cols, const float 
   }
 }
 
-// e4m3 values of a pack of y, and the scale of each block it lies in. Every lane of the warp takes
-// part (packs past the row hold zeros). A block of 32, 64 or 128 columns never leaves a warp's packs.
+// Largest magnitude of the block of each element of a pack. Every lane of the warp takes part (packs
+// past the row hold zeros). A block of 32, 64 or 128 columns never leaves a warp's packs.
 template <bool VECT, int PACK>
-__device__ __forceinline__ void store_fp8(const RmsArgs& a, long long row, int p, const float (&y)[PACK], float row_scale) {
-  float s[PACK];
-  if (a.block == 0) {
+__device__ __forceinline__ void block_tops(int block, const float (&v)[PACK], float (&top)[PACK]) {
+  if constexpr (VECT) {  // a block: block / PACK neighbouring lanes
+    float m = fabsf(v[0]);
 #pragma unroll
-    for (int e = 0; e < PACK; ++e) s[e] = row_scale;
-  } else {
-    const int nblocks = (a.cols + a.block - 1) / a.block;
-    float* out = a.scales + row * nblocks;
-    if constexpr (VECT) {  // a block: block / PACK neighbouring lanes
-      float m = 0.f;
+    for (int e = 1; e < PACK; ++e) m = max_nan(m, fabsf(v[e]));
+    top[0] = lanes_max(m, block / PACK);
+  } else {  // a block: elements e .. e + block / 32 of all 32 lanes
+    const int per = block / 32;
+    float m = 0.f;
 #pragma unroll
-      for (int e = 0; e < PACK; ++e) m = max_nan(m, fabsf(y[e]));
-      m = max_nan(lanes_max(m, a.block / PACK) / kE4m3Max, kMinScale);
+    for (int e = 0; e < PACK; ++e) {
+      m = max_nan(m, fabsf(v[e]));
+      if ((e + 1) % per == 0) {
+        m = lanes_max(m, 32);
 #pragma unroll
-      for (int e = 0; e < PACK; ++e) s[e] = m;
-      if (p * PACK < a.cols && p * PACK % a.block == 0) out[p * PACK / a.block] = m;
-    } else {  // a block: elements e .. e + block / 32 of all 32 lanes
-      const int per = a.block / 32;
-      float m = 0.f;
-#pragma unroll
-      for (int e = 0; e < PACK; ++e) {
-        m = max_nan(m, fabsf(y[e]));
-        if ((e + 1) % per == 0) {
-          m = max_nan(lanes_max(m, 32) / kE4m3Max, kMinScale);
-#pragma unroll
-          for (int f = 0; f < PACK; ++f)
-            if (f <= e && f > e - per) s[f] = m;
-          const int c = column<VECT, PACK>(p & ~31, e + 1 - per);
-          if ((p & 31) == 0 && c < a.cols) out[c / a.block] = m;
-          m = 0.f;
-        }
+        for (int f = 0; f < PACK; ++f)
+          if (f <= e && f > e - per) top[f] = m;
+        m = 0.f;
       }
     }
   }
+}
+
+__device__ __forceinline__ float scale_of(float top, float rstd) {
+  return max_nan(top * rstd * (1.0f / kE4m3Max), kMinScale);
+}
+
+// e4m3 values of a pack of h * w, and the scales of the blocks that begin in it.
+template <bool VECT, int PACK>
+__device__ __forceinline__ void store_fp8(const RmsArgs& a, long long row, int p, const float (&hw)[PACK],
+                                          const float (&top)[PACK], float rstd) {
   uint8_t* q = static_cast<uint8_t*>(a.y) + row * a.y_stride;
-#pragma unroll
-  for (int e = 0; e < PACK; ++e) s[e] = 1.0f / s[e];
+  float* out = a.scales + row * a.nblocks;
   if constexpr (VECT) {
+    const float s = scale_of(top[0], rstd), inv = __fdividef(1.0f, s);
     if (p * PACK < a.cols) {
+      if (a.block && (p * PACK & (a.block - 1)) == 0) out[p * PACK >> a.block_log2] = s;
       uint32_t w[PACK / 4];
 #pragma unroll
       for (int i = 0; i < PACK / 4; ++i)
-        w[i] = sd::rows::e4m3x2(y[4 * i] * s[0], y[4 * i + 1] * s[0]) |
-               (sd::rows::e4m3x2(y[4 * i + 2] * s[0], y[4 * i + 3] * s[0]) << 16);
+        w[i] = sd::rows::e4m3x2(hw[4 * i] * rstd * inv, hw[4 * i + 1] * rstd * inv) |
+               (sd::rows::e4m3x2(hw[4 * i + 2] * rstd * inv, hw[4 * i + 3] * rstd * inv) << 16);
       if constexpr (PACK == 8) *reinterpret_cast<uint2*>(q + p * PACK) = make_uint2(w[0], w[1]);
       else *reinterpret_cast<uint32_t*>(q + p * PACK) = w[0];
     }
@@ -167,7 +183,10 @@ __device__ __forceinline__ void store_fp8(const RmsArgs& a, long long row, int p
 #pragma unroll
     for (int e = 0; e < PACK; ++e) {
       const int c = column<VECT, PACK>(p, e);
-      if (c < a.cols) q[c] = static_cast<uint8_t>(sd::rows::e4m3x2(y[e] * s[e], 0.f));
+      if (c >= a.cols) continue;
+      const float s = scale_of(top[e], rstd);
+      if (a.block && (c & (a.block - 1)) == 0) out[c >> a.block_log2] = s;
+      q[c] = static_cast<uint8_t>(sd::rows::e4m3x2(hw[e] * rstd * __fdividef(1.0f, s), 0.f));
     }
   }
 }
@@ -176,14 +195,14 @@ __device__ __forceinline__ void store_fp8(const RmsArgs& a, long long row, int p
 template <typename T, bool FP8, bool VECT, int NV>
 __global__ void __launch_bounds__(kMaxThreads) rms_norm_kernel(const RmsArgs a, int warp_row) {
   constexpr int PACK = PackOf<T>::N;
-  __shared__ float part[32];
+  __shared__ float part[2][kMaxThreads / 32];
   sd::grid_dep_wait();
   sd::grid_dep_launch();
-  const int lane_threads = warp_row ? 32 : blockDim.x;          // threads that share a row
+  const int row_threads = warp_row ? 32 : blockDim.x;  // threads that share a row
   const int tid = warp_row ? (threadIdx.x & 31) : threadIdx.x;
-  const long long row = warp_row ? static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)
+  const long long row = warp_row ? static_cast<long long>(blockIdx.x) * kWarpRows + (threadIdx.x >> 5)
                                  : static_cast<long long>(blockIdx.x);
-  if (row >= a.rows) return;  // whole warps (warp_row), never in a CTA that shares a row
+  if (row >= a.rows) return;  // whole warps (warp_row), never a CTA that shares a row
   const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
   const T* r = a.residual ? static_cast<const T*>(a.residual) + row * a.residual_stride : nullptr;
   T* ro = a.residual_out ? static_cast<T*>(a.residual_out) + row * a.residual_out_stride : nullptr;
@@ -198,92 +217,109 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_kernel(const RmsArgs a, 
       for (int e = 0; e < PACK; ++e) h[e] += t[e];
     }
   };
-  auto weighted = [&](int p, const float (&h)[PACK], float rstd, float (&v)[PACK]) {
+  auto weighted = [&](int p, float (&h)[PACK]) {  // h * w; zeros past the row stay zeros
+    if (!a.weight) return;
     float w[PACK];
-    if (!a.weight) {
+    if (a.weight_f32) {
+      const float* f = static_cast<const float*>(a.weight);
+      if constexpr (VECT) {
+        if (p * PACK < a.cols) {
 #pragma unroll
-      for (int e = 0; e < PACK; ++e) w[e] = 1.f;
-    } else if (a.weight_f32) {
+          for (int e = 0; e < PACK; ++e) w[e] = __ldg(f + p * PACK + e);
+        } else {
 #pragma unroll
-      for (int e = 0; e < PACK; ++e) {
-        const int c = column<VECT, PACK>(p, e);
-        w[e] = c < a.cols ? __ldg(static_cast<const float*>(a.weight) + c) : 0.f;
+          for (int e = 0; e < PACK; ++e) w[e] = 0.f;
+        }
+      } else {
+        load_pack<float, VECT, PACK>(f, p, a.cols, w);
       }
     } else {
       load_pack<T, VECT, PACK>(static_cast<const T*>(a.weight), p, a.cols, w);
     }
 #pragma unroll
-    for (int e = 0; e < PACK; ++e) v[e] = column<VECT, PACK>(p, e) < a.cols ? h[e] * rstd * w[e] : 0.f;
+    for (int e = 0; e < PACK; ++e) h[e] *= w[e];
   };
+  auto rstd_of = [&](float sum) { return rsqrtf(fmaf(sum, a.inv_cols, a.eps)); };
 
   if constexpr (NV > 0) {
-    float h[NV][PACK];
-    float ss = 0.f;
+    float h[NV][PACK], top[NV][PACK];
+    float ss = 0.f, row_top = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) read(i * lane_threads + tid, h[i]);
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < PACK; ++e) ss = fmaf(h[i][e], h[i][e], ss);
-    ss = row_reduce<false>(ss, warp_row, part);
-    const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
-    if (ro) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) store_pack<T, VECT, PACK>(ro, i * lane_threads + tid, a.cols, h[i]);
-    }
-    float row_max = 0.f;
+    for (int i = 0; i < NV; ++i) read(i * row_threads + tid, h[i]);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int p = i * lane_threads + tid;
-      weighted(p, h[i], rstd, h[i]);
-      if constexpr (FP8) {
+      const int p = i * row_threads + tid;
 #pragma unroll
-        for (int e = 0; e < PACK; ++e) row_max = max_nan(row_max, fabsf(h[i][e]));
+      for (int e = 0; e < PACK; ++e) ss = fmaf(h[i][e], h[i][e], ss);
+      if (ro) store_pack<T, VECT, PACK>(ro, p, a.cols, h[i]);
+      // y = (h w) rstd with rstd the same all over the row: the magnitudes' order is that of h w, so
+      // the blocks' maxima do not wait for the row's sum.
+      weighted(p, h[i]);
+      if constexpr (FP8) {
+        if (a.block) {
+          block_tops<VECT, PACK>(a.block, h[i], top[i]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < PACK; ++e) row_top = max_nan(row_top, fabsf(h[i][e]));
+        }
+      }
+    }
+    const bool one_scale = FP8 && a.block == 0;
+    const Totals t = one_scale ? row_totals<FP8>(ss, row_top, warp_row, part) : row_totals<false>(ss, 0.f, warp_row, part);
+    const float rstd = rstd_of(t.sum);
+    if (one_scale && tid == 0) a.scales[row] = scale_of(t.top, rstd);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int p = i * row_threads + tid;
+      if constexpr (FP8) {
+        if (one_scale) {
+#pragma unroll
+          for (int e = 0; e < PACK; ++e) top[i][e] = t.top;
+        }
+        store_fp8<VECT, PACK>(a, row, p, h[i], top[i], rstd);
       } else {
+#pragma unroll
+        for (int e = 0; e < PACK; ++e) h[i][e] *= rstd;
         store_pack<T, VECT, PACK>(y, p, a.cols, h[i]);
       }
     }
-    if constexpr (FP8) {
-      float s = 1.f;
-      if (a.block == 0) {
-        s = max_nan(row_reduce<true>(row_max, warp_row, part) / kE4m3Max, kMinScale);
-        if (tid == 0) a.scales[row] = s;
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) store_fp8<VECT, PACK>(a, row, i * lane_threads + tid, h[i], s);
-    }
   } else {
-    const int chunk = lane_threads * PACK;  // columns that the row's threads take at a time
-    float ss = 0.f;
+    const int chunk = row_threads * PACK;  // columns that the row's threads take at a time
+    float ss = 0.f, row_top = 0.f;
     for (int i = 0; static_cast<long long>(i) * chunk < a.cols; ++i) {
       float h[PACK];
-      read(i * lane_threads + tid, h);
+      read(i * row_threads + tid, h);
 #pragma unroll
       for (int e = 0; e < PACK; ++e) ss = fmaf(h[e], h[e], ss);
-    }
-    ss = row_reduce<false>(ss, warp_row, part);
-    const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.cols) + a.eps);
-    float s = 1.f;
-    if (FP8 && a.block == 0) {
-      float m = 0.f;
-      for (int i = 0; static_cast<long long>(i) * chunk < a.cols; ++i) {
-        float h[PACK], v[PACK];
-        read(i * lane_threads + tid, h);
-        weighted(i * lane_threads + tid, h, rstd, v);
+      if (FP8 && a.block == 0) {
+        weighted(i * row_threads + tid, h);
 #pragma unroll
-        for (int e = 0; e < PACK; ++e) m = max_nan(m, fabsf(v[e]));
+        for (int e = 0; e < PACK; ++e) row_top = max_nan(row_top, fabsf(h[e]));
       }
-      s = max_nan(row_reduce<true>(m, warp_row, part) / kE4m3Max, kMinScale);
-      if (tid == 0) a.scales[row] = s;
     }
+    const Totals t = row_totals<FP8>(ss, row_top, warp_row, part);
+    const float rstd = rstd_of(t.sum);
+    if (FP8 && a.block == 0 && tid == 0) a.scales[row] = scale_of(t.top, rstd);
     for (int i = 0; static_cast<long long>(i) * chunk < a.cols; ++i) {
-      const int p = i * lane_threads + tid;
-      float h[PACK], v[PACK];
+      const int p = i * row_threads + tid;
+      float h[PACK];
       read(p, h);
       if (ro) store_pack<T, VECT, PACK>(ro, p, a.cols, h);
-      weighted(p, h, rstd, v);
-      if constexpr (FP8) store_fp8<VECT, PACK>(a, row, p, v, s);
-      else store_pack<T, VECT, PACK>(y, p, a.cols, v);
+      weighted(p, h);
+      if constexpr (FP8) {
+        float top[PACK];
+        if (a.block) {
+          block_tops<VECT, PACK>(a.block, h, top);
+        } else {
+#pragma unroll
+          for (int e = 0; e < PACK; ++e) top[e] = t.top;
+        }
+        store_fp8<VECT, PACK>(a, row, p, h, top, rstd);
+      } else {
+#pragma unroll
+        for (int e = 0; e < PACK; ++e) h[e] *= rstd;
+        store_pack<T, VECT, PACK>(y, p, a.cols, h);
+      }
     }
   }
 }
@@ -291,7 +327,7 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_kernel(const RmsArgs a, 
 template <typename T, bool FP8, bool VECT, int NV>
 sd_status launch(const RmsArgs& a, int threads, bool warp_row, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const long long per = warp_row ? threads / 32 : 1;
+  const long long per = warp_row ? kWarpRows : 1;
   cfg.gridDim = dim3(static_cast<unsigned>((a.rows + per - 1) / per));
   cfg.blockDim = dim3(threads);
   cfg.stream = s;
@@ -306,15 +342,19 @@ template <typename T, bool FP8, bool VECT>
 sd_status dispatch(const RmsArgs& a, cudaStream_t s) {
   constexpr int PACK = PackOf<T>::N;
   const int packs = (a.cols + 32 * PACK - 1) / (32 * PACK) * 32;  // whole warps of packs
-  // One warp per row while a warp holds the row and there are rows for eight warps on every SM; else
-  // one CTA per row with one pack a thread as far as it goes.
-  const bool warp_row = packs <= 32 * kMaxPacks && a.rows >= 8LL * sd::sm_count();
-  const int threads = warp_row ? kWarpRowThreads : std::min(packs, kMaxThreads);
-  const int nv = (packs + (warp_row ? 32 : threads) - 1) / (warp_row ? 32 : threads);
+  // Threads per row, measured in us (B200, bf16, residual; [rows, cols], e4m3 marked 8):
+  //   rows all resident at once: one pack a thread  ([300, 1280] 8: 160 threads 2.5, 96 2.8, a warp 4.1);
+  //   else narrow rows: a warp each                 ([8192, 320]: a warp 4.7, 64 threads 9.0; [8192, 640] 8: 7.2, 10.4);
+  //   else two packs a thread                       ([32760, 2048]: 128 threads 80.6, 256 92, a warp 103;
+  //                                                  [8192, 1280] 8: 96 threads 15.8, 160 18.0, a warp 16.7).
+  const bool resident = a.rows * std::min(packs, kMaxThreads) <= 2048LL * sd::sm_count();
+  const bool warp_row = !resident && packs <= 96;
+  const int one = std::min(packs, kMaxThreads), two = std::min((packs / 2 + 31) / 32 * 32, kMaxThreads);
+  const int threads = warp_row ? 32 * kWarpRows : resident ? one : two;
+  const int row_threads = warp_row ? 32 : threads, nv = (packs + row_threads - 1) / row_threads;
   if (nv <= 1) return launch<T, FP8, VECT, 1>(a, threads, warp_row, s);
   if (nv <= 2) return launch<T, FP8, VECT, 2>(a, threads, warp_row, s);
   if (nv <= 3) return launch<T, FP8, VECT, 3>(a, threads, warp_row, s);
-  if (nv <= 5) return launch<T, FP8, VECT, 5>(a, threads, warp_row, s);
   if (nv <= kMaxPacks) return launch<T, FP8, VECT, kMaxPacks>(a, threads, warp_row, s);
   return launch<T, FP8, VECT, 0>(a, threads, warp_row, s);
 }
@@ -375,6 +415,9 @@ sd_status rms_impl(const char* name, RmsArgs a, int64_t rows, int64_t cols, int 
   a.rows = rows;
   a.cols = static_cast<int>(cols);
   a.weight_f32 = weight_f32;
+  a.inv_cols = 1.0f / static_cast<float>(cols);
+  a.block_log2 = a.block == 128 ? 7 : a.block == 64 ? 6 : 5;
+  a.nblocks = static_cast<int>(nblocks);
   // 16-byte accesses want every row of every tensor to start on one, and whole packs in a row.
   const int64_t pack = 16 / size;
   auto vec = [&](const void* p, int64_t stride, int64_t align) {
