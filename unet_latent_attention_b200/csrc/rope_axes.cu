@@ -10,15 +10,19 @@
 // that is modulo whole turns: the fraction of a turn is exact at every 32-bit position, where a
 // product in fp32 is a radian off at positions of 10^7. Its upper 32 bits go to sincospi in fp32.
 //
-// Bound by HBM: q and k are read once and written once. A team of lanes holds one head of one token,
-// eight columns (four pairs) a lane, in registers; the four sines and cosines of a lane are formed
-// once per token and serve HEADS heads of q and k (at one head a thread the sine work alone would
-// take longer than the transfer), whose loads are all in flight together.
+// Bound by HBM: q and k are read once and written once. A CTA forms the sines and cosines of its
+// tokens once, one pair a thread, multiplies them with the weights and leaves them in shared memory as
+// four coefficients a pair; with them a pair of any head is turned in four operations. (Formed by each
+// head's threads for themselves they cost more than the transfer: 187 us at one head a thread against
+// 88 us for [1, 32760, 16 + 16, 128] bf16 with norm, 6130 GB/s; a plain copy reaches 6560.) A team of
+// lanes holds one head of one token at a time, eight columns (four pairs) a lane, in registers; the
+// loads of up to four heads are in flight together, the first of them while the sines are formed.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "rows_common.cuh"
 #include "sd_internal.h"
@@ -41,144 +45,262 @@ struct RopeKernelArgs {
   const int32_t* positions;            // [B, L, axes], or [L, axes] (pos_batch = 0)
   const unsigned long long* freqs;     // [rot / 2]
   long long pos_batch;
-  unsigned int L, teams, groups;       // groups: head groups of a token
+  unsigned int L, tokens, all_tokens;  // tokens of a CTA; B * L
+  int teams, q_teams;                  // teams of a token; those that take q's heads
+  int batches, k_batches;              // batches of heads that a team takes; of k, where it takes both
   int heads, kv_heads, dh, rot, axes;
   int axis_end[kMaxAxes];              // pairs before the end of each axis
-  float eps;
+  float eps, inv_dh;
+  int norms;                           // whether q or k has a weight
 };
 
-// LANES: lanes of a team, a power of two >= dh / 8. HEADS: heads a team takes, one after another.
-template <typename T, bool HALF, int LANES, int HEADS>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeKernelArgs a) {
-  sd::grid_dep_wait();
-  sd::grid_dep_launch();
-  const unsigned int team = blockIdx.x * (kThreads / LANES) + threadIdx.x / LANES;
-  const int u = threadIdx.x % LANES;  // this lane's eight columns
-  const bool live = team < a.teams;   // every lane stays for the shuffles
-  const unsigned int token = live ? team / a.groups : 0, group = live ? team % a.groups : 0;
-  const unsigned int b = token / a.L, t = token % a.L;
-  const int half = a.rot / 2;
-  const bool holds = live && u < a.dh / 8, turns = holds && u < a.rot / 8;
-  // columns of the lane's first and second four values
-  const bool split = HALF && turns;
-  const int c0 = split ? 4 * u : 8 * u, c1 = split ? half + 4 * u : 8 * u + 4;
+// The 16 bytes (two times 16 for fp32) of a lane's eight columns, as they lie in memory.
+template <typename T, bool HALF>
+struct Raw {
+  static constexpr int WORDS = sizeof(T) == 4 ? 8 : 4;
+  uint32_t w[WORDS];
 
-  // Loads first: the angles are formed while they are on their way.
-  float v[HEADS][8];
-#pragma unroll
-  for (int i = 0; i < HEADS; ++i) {
-    const int h = static_cast<int>(group + i * a.groups);  // neighbouring teams take neighbouring heads
-    const bool is_q = h < a.heads;
-    if (holds && h < a.heads + a.kv_heads) {
-      const RopeTensor& x = is_q ? a.q : a.k;
-      const T* p = static_cast<const T*>(x.in) + b * x.in_batch + t * x.in_token + (is_q ? h : h - a.heads) * x.in_head;
+  __device__ __forceinline__ void load(const T* p, int c0, int c1) {
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p + c0);
+      *reinterpret_cast<uint4*>(w + 4) = *reinterpret_cast<const uint4*>(p + c1);
+    } else if constexpr (HALF) {
+      *reinterpret_cast<uint2*>(w) = *reinterpret_cast<const uint2*>(p + c0);
+      *reinterpret_cast<uint2*>(w + 2) = *reinterpret_cast<const uint2*>(p + c1);
+    } else {
+      *reinterpret_cast<uint4*>(w) = *reinterpret_cast<const uint4*>(p + c0);
+    }
+  }
+  // First (x) and second (y) values of the pairs: x[i] holds those of pairs 2i and 2i + 1, for packed
+  // arithmetic. Where the lane's columns do not turn, value i of the first (second) four is the same
+  // slot of x (y).
+  __device__ __forceinline__ void get(float2 (&x)[2], float2 (&y)[2]) const {
+    if constexpr (sizeof(T) == 4) {
+      const float f[8] = {__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]),
+                          __uint_as_float(w[4]), __uint_as_float(w[5]), __uint_as_float(w[6]), __uint_as_float(w[7])};
       if constexpr (HALF) {
-        float lo[4], hi[4];
-        sd::rows::load(p + c0, lo);
-        sd::rows::load(p + c1, hi);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[i][e] = lo[e], v[i][4 + e] = hi[e];
+        x[0] = make_float2(f[0], f[1]), x[1] = make_float2(f[2], f[3]);
+        y[0] = make_float2(f[4], f[5]), y[1] = make_float2(f[6], f[7]);
       } else {
-        sd::rows::load(p + c0, v[i]);
+        x[0] = make_float2(f[0], f[2]), x[1] = make_float2(f[4], f[6]);
+        y[0] = make_float2(f[1], f[3]), y[1] = make_float2(f[5], f[7]);
       }
     } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = 0.f;
-    }
-  }
-
-  float cs[4], sn[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) cs[e] = 1.f, sn[e] = 0.f;
-  if (turns) {
-    const int32_t* pos = a.positions + b * a.pos_batch + static_cast<long long>(t) * a.axes;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int m = 4 * u + e;
-      int axis = 0;
-#pragma unroll
-      for (int i = 0; i + 1 < kMaxAxes; ++i) axis += (i + 1 < a.axes && m >= a.axis_end[i]) ? 1 : 0;
-      const unsigned long long f = __ldg(a.freqs + m);
-      const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(__ldg(pos + axis))) * f;
-      // the upper 32 bits as a signed fraction: half turns in [-1, 1)
-      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &sn[e], &cs[e]);
-    }
-  }
-
-#pragma unroll
-  for (int i = 0; i < HEADS; ++i) {
-    const int h = static_cast<int>(group + i * a.groups);
-    const bool is_q = h < a.heads, there = holds && h < a.heads + a.kv_heads;
-    const RopeTensor& x = is_q ? a.q : a.k;
-    if (a.q.weight || a.k.weight) {  // the same for the whole grid: every lane takes part in the sum
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(v[i][e], v[i][e], ss);
-#pragma unroll
-      for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (there && x.weight) {
-        const float rstd = 1.0f / sqrtf(ss / static_cast<float>(a.dh) + a.eps);
-        const float4 w0 = *reinterpret_cast<const float4*>(x.weight + c0);
-        const float4 w1 = *reinterpret_cast<const float4*>(x.weight + c1);
-        v[i][0] *= rstd * w0.x, v[i][1] *= rstd * w0.y, v[i][2] *= rstd * w0.z, v[i][3] *= rstd * w0.w;
-        v[i][4] *= rstd * w1.x, v[i][5] *= rstd * w1.y, v[i][6] *= rstd * w1.z, v[i][7] *= rstd * w1.w;
-      }
-    }
-    if (!there) continue;
-    float r[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int p0 = split ? e : 2 * e, p1 = split ? 4 + e : 2 * e + 1;
-      const float x0 = HALF ? (split ? v[i][e] : v[i][2 * e]) : v[i][2 * e];
-      const float x1 = HALF ? (split ? v[i][4 + e] : v[i][2 * e + 1]) : v[i][2 * e + 1];
-      const float y0 = fmaf(x0, cs[e], -x1 * sn[e]), y1 = fmaf(x0, sn[e], x1 * cs[e]);
-      if (HALF) {
-        if (split) r[e] = y0, r[4 + e] = y1;
-        else r[2 * e] = y0, r[2 * e + 1] = y1;
+      const float2 a = sd::rows::unpack2<T>(w[0]), b = sd::rows::unpack2<T>(w[1]), c = sd::rows::unpack2<T>(w[2]),
+                   d = sd::rows::unpack2<T>(w[3]);
+      if constexpr (HALF) {
+        x[0] = a, x[1] = b, y[0] = c, y[1] = d;
       } else {
-        r[p0] = y0, r[p1] = y1;
+        x[0] = make_float2(a.x, b.x), x[1] = make_float2(c.x, d.x);
+        y[0] = make_float2(a.y, b.y), y[1] = make_float2(c.y, d.y);
       }
     }
-    if (!turns) {  // columns behind the rotated ones pass (an infinity must not meet a zero sine)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) r[e] = v[i][e];
-    }
-    T* p = static_cast<T*>(x.out) + b * x.out_batch + t * x.out_token + (is_q ? h : h - a.heads) * x.out_head;
+  }
+  __device__ __forceinline__ static void store(T* p, int c0, int c1, const float2 (&x)[2], const float2 (&y)[2]) {
     if constexpr (HALF) {
-      const float lo[4] = {r[0], r[1], r[2], r[3]}, hi[4] = {r[4], r[5], r[6], r[7]};
+      const float lo[4] = {x[0].x, x[0].y, x[1].x, x[1].y}, hi[4] = {y[0].x, y[0].y, y[1].x, y[1].y};
       sd::rows::store(p + c0, lo);
       sd::rows::store(p + c1, hi);
     } else {
-      sd::rows::store(p + c0, r);
+      const float v[8] = {x[0].x, y[0].x, x[0].y, y[0].y, x[1].x, y[1].x, x[1].y, y[1].y};
+      sd::rows::store(p + c0, v);
+    }
+  }
+};
+
+// The heads of one tensor that a team turns: first, first + step, ... below heads. The lane's
+// coefficients of its four pairs are c[e] = (w0 cos, w0 sin, w1 cos, -w1 sin).
+template <typename T, bool HALF, int LANES, bool NORM, int kBatch>
+struct Rows {
+  const T* in;
+  T* out;
+  long long in_step, out_step;
+  int left;  // heads still to come, the same for all lanes of a warp's teams or less
+  bool holds, turns, norm;
+  int c0, c1;
+  Raw<T, HALF> raw[kBatch];
+
+  __device__ __forceinline__ void init(const RopeTensor& x, bool there, unsigned int b, unsigned int t, int first, int step,
+                                       int heads) {
+    in = static_cast<const T*>(x.in) + b * x.in_batch + t * x.in_token + first * x.in_head;
+    out = static_cast<T*>(x.out) + b * x.out_batch + t * x.out_token + first * x.out_head;
+    in_step = step * x.in_head, out_step = step * x.out_head;
+    left = there ? (heads - first + step - 1) / step : 0;
+    norm = NORM && x.weight != nullptr;
+  }
+  __device__ __forceinline__ void load() {  // the next batch
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (holds && i < left) {
+        raw[i].load(in, c0, c1);
+      } else {
+#pragma unroll
+        for (int e = 0; e < Raw<T, HALF>::WORDS; ++e) raw[i].w[e] = 0;
+      }
+      in += in_step;
+    }
+  }
+  __device__ __forceinline__ void turn(const RopeKernelArgs& a, const float4 (&c)[4]) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      float2 vx[2], vy[2];
+      raw[i].get(vx, vy);
+      float x[4] = {vx[0].x, vx[0].y, vx[1].x, vx[1].y}, y[4] = {vy[0].x, vy[0].y, vy[1].x, vy[1].y};
+      float rstd = 1.f;
+      if constexpr (NORM) {  // every lane takes part in the sum
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ss = fmaf(x[e], x[e], fmaf(y[e], y[e], ss));
+#pragma unroll
+        for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (norm) rstd = rsqrtf(fmaf(ss, a.inv_dh, a.eps));
+      }
+      if (holds && i < left) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float p, q;
+          if (turns) {
+            p = fmaf(x[e], c[e].x, y[e] * c[e].w);
+            q = fmaf(x[e], c[e].y, y[e] * c[e].z);
+          } else {  // columns behind the rotated ones (an infinity must not meet a zero sine)
+            p = x[e] * c[e].x;
+            q = y[e] * c[e].z;
+          }
+          x[e] = NORM ? p * rstd : p;
+          y[e] = NORM ? q * rstd : q;
+        }
+        const float2 rx[2] = {{x[0], x[1]}, {x[2], x[3]}}, ry[2] = {{y[0], y[1]}, {y[2], y[3]}};
+        Raw<T, HALF>::store(out, c0, c1, rx, ry);
+      }
+      out += out_step;
+    }
+    left -= kBatch;
+  }
+};
+
+// LANES: lanes of a team, a power of two >= dh / 8. NORM: whether q or k has a weight. A CTA turns all
+// heads of a.tokens tokens, a.teams teams to a token: each takes some of q's and some of k's (BOTH), or
+// a.q_teams of them take q's heads and the others k's.
+template <typename T, bool HALF, int LANES, bool NORM, int kBatch, bool BOTH>
+__global__ void __launch_bounds__(kThreads, !BOTH || sizeof(T) == 4 ? 1 : HALF ? 3 : 4) rope_kernel(const __grid_constant__ RopeKernelArgs a) {
+  extern __shared__ float4 coef[];  // [q, k if NORM][tokens][4][LANES]
+  sd::grid_dep_wait();
+  sd::grid_dep_launch();
+  const int u = threadIdx.x % LANES, team = threadIdx.x / LANES;
+  const int slot = team / a.teams, j = team % a.teams;  // this team's token of the CTA, and its place there
+  const unsigned int token = blockIdx.x * a.tokens + slot;
+  const bool there = slot < static_cast<int>(a.tokens) && token < a.all_tokens;
+  const unsigned int b = there ? token / a.L : 0, t = there ? token % a.L : 0;
+  Rows<T, HALF, LANES, NORM, kBatch> rows;
+  rows.holds = u < a.dh / 8;
+  rows.turns = u < a.rot / 8;
+  // columns of the lane's first and second four values in memory
+  const bool split = HALF && rows.turns;
+  rows.c0 = split ? 4 * u : 8 * u, rows.c1 = split ? a.rot / 2 + 4 * u : 8 * u + 4;
+  const bool on_k = !BOTH && j >= a.q_teams;
+  if (on_k) rows.init(a.k, there && j - a.q_teams < a.kv_heads, b, t, j - a.q_teams, a.teams - a.q_teams, a.kv_heads);
+  else rows.init(a.q, there && j < a.heads, b, t, j, a.q_teams, a.heads);
+  rows.load();  // on its way while the coefficients are formed
+
+  for (int i = threadIdx.x; i < static_cast<int>(a.tokens) * 4 * LANES; i += kThreads) {
+    const int lane = i % LANES, e = i / LANES % 4, k = i / (4 * LANES);  // pair 4 * lane + e of token k
+    const unsigned int tok = blockIdx.x * a.tokens + k;
+    if (lane >= a.dh / 8 || tok >= a.all_tokens) continue;
+    float s = 0.f, c = 1.f;
+    const int m = 4 * lane + e;
+    const bool pair = lane < a.rot / 8;
+    if (pair) {
+      int axis = 0;
+#pragma unroll
+      for (int n = 0; n + 1 < kMaxAxes; ++n) axis += (n + 1 < a.axes && m >= a.axis_end[n]) ? 1 : 0;
+      const unsigned int tb = tok / a.L, tt = tok % a.L;
+      const int p = __ldg(a.positions + tb * a.pos_batch + static_cast<long long>(tt) * a.axes + axis);
+      const unsigned long long turn = static_cast<unsigned long long>(static_cast<long long>(p)) * __ldg(a.freqs + m);
+      // the upper 32 bits as a signed fraction: half turns in [-1, 1)
+      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 4.656612873077393e-10f, &s, &c);
+    }
+    if constexpr (NORM) {
+      // columns of the pair's two values; behind the rotated ones, of the slots of x and y (see Raw)
+      const int m0 = HALF ? (pair ? m : 8 * lane + e) : 2 * m, m1 = HALF ? (pair ? m + a.rot / 2 : 8 * lane + 4 + e) : 2 * m + 1;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        const float* w = n ? a.k.weight : a.q.weight;
+        const float w0 = w ? __ldg(w + m0) : 1.f, w1 = w ? __ldg(w + m1) : 1.f;
+        coef[((n * a.tokens + k) * 4 + e) * LANES + lane] = make_float4(w0 * c, w0 * s, w1 * c, -w1 * s);
+      }
+    } else {
+      coef[(k * 4 + e) * LANES + lane] = make_float4(c, s, c, -s);
+    }
+  }
+  __syncthreads();
+
+  float4 c[4];
+  const float4* mine = coef + (there ? slot : 0) * 4 * LANES + u;
+  const int k_coef = NORM ? a.tokens * 4 * LANES : 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c[e] = mine[(on_k ? k_coef : 0) + e * LANES];
+  for (int n = 0; n < a.batches; ++n) {  // the same number for every warp of the grid
+    if (n) rows.load();
+    rows.turn(a, c);
+  }
+  if (BOTH && a.kv_heads) {
+    rows.init(a.k, there && j < a.kv_heads, b, t, j, a.teams, a.kv_heads);
+    if constexpr (NORM) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) c[e] = mine[k_coef + e * LANES];
+    }
+    for (int n = 0; n < a.k_batches; ++n) {
+      rows.load();
+      rows.turn(a, c);
     }
   }
 }
 
-template <typename T, bool HALF, int LANES, int HEADS>
-sd_status launch(RopeKernelArgs a, int64_t tokens, cudaStream_t s) {
-  a.groups = static_cast<unsigned>((a.heads + a.kv_heads + HEADS - 1) / HEADS);
-  const int64_t teams = tokens * a.groups;
-  const int64_t blocks = (teams + kThreads / LANES - 1) / (kThreads / LANES);
-  if (teams > 0xffffffffLL - kThreads || blocks > 0x7fffffff)
-    return sd::fail(SD_ERR_UNSUPPORTED, "sd_rope_axes: too many heads and tokens");
-  a.teams = static_cast<unsigned>(teams);
+template <typename T, bool HALF, int LANES, bool NORM, int BATCH, bool BOTH>
+sd_status launch(RopeKernelArgs a, int64_t tokens, int per, cudaStream_t s) {
+  auto batches = [](int heads, int teams) { return teams ? (heads + BATCH * teams - 1) / (BATCH * teams) : 0; };
+  a.tokens = per;
+  a.teams = kThreads / LANES / per;
+  a.all_tokens = static_cast<unsigned>(tokens);
+  const int heads = a.heads + a.kv_heads;
+  a.q_teams = a.teams;
+  if (!BOTH && a.heads && a.kv_heads && a.teams > 1)  // none has much more to do than another
+    a.q_teams = std::min(std::max((a.teams * a.heads + heads / 2) / heads, 1), a.teams - 1);
+  a.batches = std::max(batches(a.heads, a.q_teams), batches(a.kv_heads, a.teams - a.q_teams));
+  a.k_batches = batches(a.kv_heads, a.teams);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.gridDim = dim3(static_cast<unsigned>((tokens + per - 1) / per));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(per) * 4 * LANES * sizeof(float4) * (NORM ? 2 : 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   cfg.attrs = attr;
   cfg.numAttrs = sd::pdl_attr(&attr[0]);
-  return sd::cuda_check(cudaLaunchKernelEx(&cfg, rope_kernel<T, HALF, LANES, HEADS>, a), "sd_rope_axes launch");
+  return sd::cuda_check(cudaLaunchKernelEx(&cfg, rope_kernel<T, HALF, LANES, NORM, BATCH, BOTH>, a), "sd_rope_axes launch");
 }
 
 template <typename T, bool HALF, int LANES>
 sd_status by_heads(const RopeKernelArgs& a, int64_t tokens, cudaStream_t s) {
-  // Four heads a thread once that still leaves every SM its 2048 threads; below, one: the call is
-  // then as long as one thread's chain of loads and stores.
-  const int64_t threads = tokens * (a.heads + a.kv_heads) * LANES;
-  return threads >= 4LL * 2048 * sd::sm_count() ? launch<T, HALF, LANES, 4>(a, tokens, s)
-                                                : launch<T, HALF, LANES, 1>(a, tokens, s);
+  // Tokens of a CTA: as many as leave two CTAs an SM and give a team no more than 20 heads. Measured
+  // (us, bf16, norm): [1, 32760, 16 + 16, 128] 4 / 8 / 16 tokens: 91.8 / 86.0 / 91.7; [2, 4173, 16 + 16,
+  // 64]: 19.6 / 13.6 / 12.7; [2, 1024, 8 + 8, 40]: 5.6 / 4.2 / 4.3.
+  // Teams with eight heads and more take some of q and some of k, which keeps a thread within the 64
+  // registers of four CTAs an SM (80 and three where half-pairs would spill: 58.4 against 63.2 us for [1,
+  // 32760, 16 + 4, 128] without norm; 87.6 and 13.1 us for the first two above, 103 and 17.9 with teams of
+  // their own for q and k). With fewer heads q and k go to different teams and are loaded at the same
+  // time ([2, 512, 16 + 4, 128]: 4.5 against 6.1).
+  constexpr int kTeams = kThreads / LANES;
+  const int heads = a.heads + a.kv_heads;
+  int per = 1;
+  while (2 * per <= kTeams && tokens / (2 * per) >= 2LL * sd::sm_count() && heads * 2 * per <= 20 * kTeams) per *= 2;
+  const int rows = (heads * per + kTeams - 1) / kTeams;  // heads of a team
+  auto pick = [&](auto norm) {
+    constexpr bool N = decltype(norm)::value;
+    if (rows >= 8) return launch<T, HALF, LANES, N, 4, true>(a, tokens, per, s);
+    if (rows >= 4) return launch<T, HALF, LANES, N, 2, false>(a, tokens, per, s);
+    return launch<T, HALF, LANES, N, 1, false>(a, tokens, per, s);
+  };
+  return a.norms ? pick(std::true_type()) : pick(std::false_type());
 }
 
 template <typename T, bool HALF>
@@ -314,7 +436,8 @@ extern "C" sd_status sd_rope_axes(const sd_rope_args* p, void* stream) {
   a.L = static_cast<unsigned>(g.L);
   a.heads = static_cast<int>(g.heads), a.kv_heads = static_cast<int>(g.kv_heads);
   a.dh = static_cast<int>(g.dh), a.rot = static_cast<int>(rot), a.axes = g.axes;
-  a.eps = g.eps;
+  a.eps = g.eps, a.inv_dh = 1.0f / static_cast<float>(g.dh);
+  a.norms = (g.heads && g.q_weight) || (g.kv_heads && g.k_weight);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t tokens = g.B * g.L;
   auto typed = [&](auto v) {
