@@ -24,6 +24,7 @@ import ctypes
 import math
 import os
 import re
+import struct
 
 from .rope import rope_frequencies  # noqa: F401
 from .schedule import (ddim_schedule, dpmpp_2m_schedule, dpmpp_3m_schedule, karras_alpha_bars,  # noqa: F401
@@ -46,22 +47,12 @@ class SDError(RuntimeError):
         super().__init__(f"{func}: {STATUS_NAMES.get(status, status)}: {detail}")
 
 
-class _RopeArgs(ctypes.Structure):  # sd_rope_args
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "q_out", "k_out", "q_weight", "k_weight", "positions", "freqs")]
-                + [(n, ctypes.c_int64) for n in ("B", "L", "heads", "kv_heads", "dh")]
-                + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
-                + [("positions_batch_stride", ctypes.c_int64), ("axis_dims", ctypes.c_int32 * 4)]
-                + [(n, ctypes.c_int32) for n in ("axes", "pairs", "dtype")] + [("eps", ctypes.c_float)])
-
-
-class _AttentionMaskedArgs(ctypes.Structure):  # sd_attention_masked_args
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "bias", "kv_lens", "q_starts", "prefix_lens",
-                                                "q_offsets", "k_offsets")]
-                + [(n, ctypes.c_int64) for n in ("B", "heads", "kv_heads", "Lq", "Lk", "dh")]
-                + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride", "o_stride")]
-                + [(n, ctypes.c_int64) for n in ("bias_radius", "docs")]
-                + [(n, ctypes.c_int32) for n in ("causal", "dtype")]
-                + [(n, ctypes.c_float) for n in ("scale", "cap")])
+# Layouts of the argument structs of include/sd_kernels.h (packed bytes cost a call far less than
+# filling a ctypes.Structure field by field).
+# sd_rope_args: 8 pointers, B .. dh, 4 x 3 strides, positions_batch_stride, axis_dims[4], axes, pairs, dtype, eps
+_ROPE_ARGS = struct.Struct("@8P5q12qq4i3if")
+# sd_attention_masked_args: 10 pointers, B .. dh, 4 x 3 strides, bias_radius, docs, causal, dtype, scale, cap
+_ATTENTION_MASKED_ARGS = struct.Struct("@10P6q12q2q2i2f")
 
 
 _lib = None
@@ -86,8 +77,8 @@ def lib() -> ctypes.CDLL:
         L.sd_cfg_dpmpp_3m_step.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, f32, f64, f64, f64, f64, vp]
         L.sd_rms_norm.argtypes = [vp] * 5 + [i64] * 6 + [f32, c_int, c_int, vp]
         L.sd_rms_norm_fp8.argtypes = [vp] * 6 + [i64] * 6 + [f32, c_int, c_int, c_int, vp]
-        L.sd_rope_axes.argtypes = [ctypes.POINTER(_RopeArgs), vp]
-        L.sd_attention_masked.argtypes = [ctypes.POINTER(_AttentionMaskedArgs), vp]
+        L.sd_rope_axes.argtypes = [ctypes.c_char_p, vp]
+        L.sd_attention_masked.argtypes = [ctypes.c_char_p, vp]
         L.sd_device_status.argtypes = [vp, c_int]
         L.sd_debug_set_fault.argtypes = [c_int]
         L.sd_debug_set_fault.restype = None
@@ -300,39 +291,41 @@ def sd_cfg_dpmpp_3m_step(x, eps_u, eps_c, d_prev, d_prev2, w: float, alpha_prev2
     return out, d_out
 
 
-def _same_cuda_device(*ts):
-    """The device of CUDA tensors that may be strided views; None entries are skipped."""
-    dev = None
-    for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("sd kernels run on CUDA tensors only (no CPU fallback)")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError("all tensors must be on one CUDA device")
+def _device_index(tensors) -> int:
+    """The index of the CUDA device that holds all ``tensors`` (None entries are skipped; views may be strided)."""
+    dev = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0 or not t.is_cuda:
+                raise ValueError("sd kernels run on CUDA tensors only (no CPU fallback)")
+            if d != dev:
+                if dev >= 0:
+                    raise ValueError("all tensors must be on one CUDA device")
+                dev = d
     return dev
 
 
-def _call(name, dev, *args) -> None:
-    """One library call on the current stream of ``dev``, with ``dev`` as the current device."""
+def _call(name, dev: int, *args) -> None:
+    """One library call on the current stream of device ``dev``, with ``dev`` as the current device."""
     import torch
-    f = getattr(lib(), name)
-    if torch.cuda.current_device() == dev.index:
-        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    f = getattr(_lib or lib(), name)
+    if torch._C._cuda_getDevice() == dev:
+        st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
-            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
     if st != SD_OK:
         _check(name, st)
 
 
-def _rows(t, name):
-    """(number of rows, elements between rows) of a tensor whose last dimension is contiguous."""
+def _ptr(t) -> int:
+    return 0 if t is None else t.data_ptr()
+
+
+def _row_stride(t, name):
+    """Elements between the rows of a tensor whose last dimension is contiguous."""
     C = t.shape[-1]
-    if t.is_contiguous():
-        return (t.numel() // C if C else 0), C
     if C > 1 and t.stride(-1) != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
     n, step = 1, None
@@ -344,7 +337,7 @@ def _rows(t, name):
         elif stride != step * n:
             raise ValueError(f"the rows of {name} must be equally far apart")
         n *= size
-    return (n if t.numel() else 0), (C if step is None else step)
+    return C if step is None else step
 
 
 _DTYPE_CODES = {}
@@ -363,33 +356,31 @@ def _dtype_code(t, func):
 def _rms(func, x, weight, eps, residual, out, residual_out, scales, block):
     import torch
     code = _dtype_code(x, func)
-    if x.dim() < 1:
-        raise ValueError("x must have at least one dimension")
-    C = x.shape[-1]
-    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
-        raise ValueError("residual must have the shape and type of x")
-    if residual_out is not None and residual is None:
+    shape, dtype = x.shape, x.dtype
+    C = shape[-1]
+    if residual is not None:
+        if residual.shape != shape or residual.dtype != dtype:
+            raise ValueError("residual must have the shape and type of x")
+        if residual_out is None:
+            residual_out = torch.empty_like(residual) if residual.is_contiguous() else torch.empty(shape, dtype=dtype, device=x.device)
+        elif residual_out.shape != shape or residual_out.dtype != dtype:
+            raise ValueError("residual_out must have the shape and type of x")
+    elif residual_out is not None:
         raise ValueError("residual_out needs residual")
-    if residual is not None and residual_out is None:
-        residual_out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if residual_out is not None and (residual_out.shape != x.shape or residual_out.dtype != x.dtype):
-        raise ValueError("residual_out must have the shape and type of x")
     wf32 = 1
     if weight is not None:
-        if weight.shape != (C,) or weight.dtype not in (torch.float32, x.dtype) or not weight.is_contiguous():
-            raise ValueError("weight must be [C], contiguous, fp32 or of the type of x")
         wf32 = int(weight.dtype == torch.float32)
-    dev = _same_cuda_device(x, weight, residual, out, residual_out, scales)
-    rows, xs = _rows(x, "x")
-    rs = _rows(residual, "residual")[1] if residual is not None else C
-    ros = _rows(residual_out, "residual_out")[1] if residual_out is not None else C
-    ys = _rows(out, "out")[1]
-    ptr = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
+        if weight.shape != (C,) or not (wf32 or weight.dtype == dtype) or not weight.is_contiguous():
+            raise ValueError("weight must be [C], contiguous, fp32 or of the type of x")
+    dev = _device_index((x, weight, residual, out, residual_out, scales))
+    rows = x.numel() // C if C else 0
+    xs, rs, ys, ros = (C if t is None or t.is_contiguous() else _row_stride(t, name) for t, name in
+                       ((x, "x"), (residual, "residual"), (out, "out"), (residual_out, "residual_out")))
     if scales is None:
-        _call(func, dev, x.data_ptr(), ptr(residual), ptr(weight), out.data_ptr(), ptr(residual_out), rows, C, xs, rs, ys,
+        _call(func, dev, x.data_ptr(), _ptr(residual), _ptr(weight), out.data_ptr(), _ptr(residual_out), rows, C, xs, rs, ys,
               ros, eps, code, wf32)
     else:
-        _call(func, dev, x.data_ptr(), ptr(residual), ptr(weight), out.data_ptr(), scales.data_ptr(), ptr(residual_out),
+        _call(func, dev, x.data_ptr(), _ptr(residual), _ptr(weight), out.data_ptr(), scales.data_ptr(), _ptr(residual_out),
               rows, C, xs, rs, ys, ros, eps, code, wf32, block)
     return residual_out
 
@@ -401,8 +392,10 @@ def sd_rms_norm(x, weight=None, eps: float = 1e-6, residual=None, out=None, resi
     residual_out = x + residual where a residual is given. ``out`` and ``residual_out`` may be ``x`` or
     ``residual`` (in place); rows may be strided, columns are contiguous."""
     import torch
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = torch.empty_like(x) if x.is_contiguous() else torch.empty(x.shape, dtype=x.dtype, device=x.device)
     elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must have the shape and type of x")
     ro = _rms("sd_rms_norm", x, weight, float(eps), residual, out, residual_out, None, 0)
@@ -417,7 +410,9 @@ def sd_rms_norm_fp8(x, weight=None, eps: float = 1e-6, residual=None, block: int
     import torch
     if block not in (0, 32, 64, 128):
         raise ValueError("block must be 0, 32, 64 or 128")
-    C = x.shape[-1] if x.dim() else 0
+    if x.dim() < 1:
+        raise ValueError("x must have at least one dimension")
+    C = x.shape[-1]
     shape = (*x.shape[:-1], -(-C // block) if block else 1)
     if out is None:
         out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
@@ -472,34 +467,26 @@ def sd_rope_axes(q, k, positions, freqs, axis_dims, pairs: str = "interleaved", 
     for w in (q_weight, k_weight):
         if w is not None and (w.dtype != torch.float32 or w.shape != (dh,) or not w.is_contiguous()):
             raise ValueError("q_weight and k_weight must be contiguous fp32 [dh]")
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-    if q_out.shape != q.shape or q_out.dtype != q.dtype:
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    elif q_out.shape != q.shape or q_out.dtype != q.dtype:
         raise ValueError("q_out must have the shape and type of q")
     if k is None:
         if k_out is not None:
             raise ValueError("k_out needs k")
-    else:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device) if k_out is None else k_out
-        if k_out.shape != k.shape or k_out.dtype != k.dtype:
-            raise ValueError("k_out must have the shape and type of k")
-    dev = _same_cuda_device(q, k, positions, freqs, q_weight, k_weight, q_out, k_out)
-    a = _RopeArgs()
-    a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
-    a.q_stride, a.q_out_stride = _strides(q, blhd, "q"), _strides(q_out, blhd, "q_out")
-    if k is not None:
-        a.k, a.k_out = k.data_ptr(), k_out.data_ptr()
-        a.k_stride, a.k_out_stride = _strides(k, blhd, "k"), _strides(k_out, blhd, "k_out")
-        a.kv_heads = k.shape[2 if blhd else 1]
-    if q_weight is not None:
-        a.q_weight = q_weight.data_ptr()
-    if k_weight is not None:
-        a.k_weight = k_weight.data_ptr()
-    a.positions, a.freqs = positions.data_ptr(), freqs.data_ptr()
-    a.B, a.L, a.heads, a.dh = B, L, H, dh
-    a.positions_batch_stride = L * axes if positions.dim() == 3 else 0
-    for i, d in enumerate(axis_dims):
-        a.axis_dims[i] = d
-    a.axes, a.pairs, a.dtype, a.eps = axes, int(pairs == "half"), code, eps
+    elif k_out is None:
+        k_out = torch.empty_like(k)
+    elif k_out.shape != k.shape or k_out.dtype != k.dtype:
+        raise ValueError("k_out must have the shape and type of k")
+    dev = _device_index((q, k, positions, freqs, q_weight, k_weight, q_out, k_out))
+    k_there = k is not None
+    dims = tuple(axis_dims)
+    a = _ROPE_ARGS.pack(
+        q.data_ptr(), k.data_ptr() if k_there else 0, q_out.data_ptr(), k_out.data_ptr() if k_there else 0, _ptr(q_weight),
+        _ptr(k_weight), positions.data_ptr(), freqs.data_ptr(), B, L, H, k.shape[2 if blhd else 1] if k_there else 0, dh,
+        *_strides(q, blhd, "q"), *(_strides(k, blhd, "k") if k_there else (0, 0, 0)), *_strides(q_out, blhd, "q_out"),
+        *(_strides(k_out, blhd, "k_out") if k_there else (0, 0, 0)), L * axes if positions.dim() == 3 else 0,
+        *dims, *(0, 0, 0)[axes - 1:], axes, pairs == "half", code, eps)
     _call("sd_rope_axes", dev, a)
     return q_out, k_out
 
@@ -561,27 +548,15 @@ def sd_attention_masked(q, k, v, scale: float | None = None, layout: str = "bhld
             raise ValueError("bias must be contiguous fp32 [heads, 2 R + 1]")
         radius = bias.shape[1] // 2
     if out is None:
-        make = torch.zeros if docs else torch.empty
-        out = make(q.shape, dtype=q.dtype, device=q.device)
-    if out.shape != q.shape or out.dtype != q.dtype:
+        out = torch.zeros_like(q) if docs else torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have the shape and type of q")
-    dev = _same_cuda_device(q, k, v, out, bias, kv_lens, q_starts, prefix_lens, q_offsets, k_offsets)
-    a = _AttentionMaskedArgs()
-    a.q, a.k, a.v, a.o = q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr()
-    a.q_stride, a.k_stride = _strides(q, blhd, "q"), _strides(k, blhd, "k")
-    a.v_stride, a.o_stride = _strides(v, blhd, "v"), _strides(out, blhd, "out")
-    a.B, a.heads, a.kv_heads, a.Lq, a.Lk, a.dh = B, H, KV, Lq, Lk, dh
-    if bias is not None:
-        a.bias, a.bias_radius = bias.data_ptr(), radius
-    if kv_lens is not None:
-        a.kv_lens = kv_lens.data_ptr()
-    if q_starts is not None:
-        a.q_starts = q_starts.data_ptr()
-    if prefix_lens is not None:
-        a.prefix_lens = prefix_lens.data_ptr()
-    if docs:
-        a.q_offsets, a.k_offsets, a.docs = q_offsets.data_ptr(), k_offsets.data_ptr(), docs
-    a.causal, a.dtype, a.scale, a.cap = int(bool(causal)), code, 1.0 / math.sqrt(dh) if scale is None else scale, cap
+    dev = _device_index((q, k, v, out, bias, kv_lens, q_starts, prefix_lens, q_offsets, k_offsets))
+    a = _ATTENTION_MASKED_ARGS.pack(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(bias), _ptr(kv_lens), _ptr(q_starts), _ptr(prefix_lens),
+        _ptr(q_offsets), _ptr(k_offsets), B, H, KV, Lq, Lk, dh, *_strides(q, blhd, "q"), *_strides(k, blhd, "k"),
+        *_strides(v, blhd, "v"), *_strides(out, blhd, "out"), radius, docs, bool(causal), code,
+        1.0 / math.sqrt(dh) if scale is None else scale, cap)
     _call("sd_attention_masked", dev, a)
     return out
 
