@@ -31,6 +31,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "sd_internal.h"
@@ -121,8 +122,9 @@ struct Cfg {
   static constexpr int BIAS_OFF = V_OFF + STAGES * KV_TILE;
   static constexpr int WINDOW = NQ * BM + BN;  // values of one bias window (one unused)
   static constexpr int BAR_OFF = BIAS_OFF + (BIAS ? STAGES * WINDOW * 4 : 0);
-  // q_full, k_full[S], v_full[S], v_ready[S], kv_empty[S], bias_full[S], s_full, s_free, p_full, o_done, fin [NQ]
-  static constexpr int NBARS = 1 + 5 * STAGES + 5 * NQ;
+  // q_full, k_full[S], v_full[S], v_ready[S], kv_empty[S], bias_full[S], s_full, s_free, p_full, o_done, fin [NQ],
+  // turn[NQ][4]
+  static constexpr int NBARS = 1 + 5 * STAGES + 9 * NQ;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // TMEM address, abort flag, cleaned flag, mixed flag
   static constexpr int BOUNDS_OFF = MISC_OFF + 16;      // per query tile: lo of its first and last row, hi of both
   static constexpr int SMEM = BOUNDS_OFF + NQ * 16 + 1024;
@@ -133,6 +135,7 @@ struct Cfg {
   static constexpr int REG_HELPER = 120, REG_SOFT = 192;
   // Of every 8 column pairs this many take exp2 on the FMA pipe; with a cap or bias that pipe has other work.
   static constexpr int POLY = CAP || BIAS ? 0 : 2;
+  static constexpr int PASS = BN / 4;  // column pairs (of BN / 2) after which a warp passes its turn on
   // Join of a cluster's parts: rows of DHT fp32 and (m, l), over the K/V ring.
   static constexpr int JOIN_ROW = DHT + 4;  // floats a row (+4: rows start in different banks)
   static_assert(TM_COLS <= 512 && SMEM <= 227 * 1024, "on-chip memory");
@@ -154,6 +157,7 @@ struct Bars {
   __device__ uint32_t p_full(int t) const { return base + 8 * (1 + 5 * S + 2 * nq + t); }
   __device__ uint32_t o_done(int t) const { return base + 8 * (1 + 5 * S + 3 * nq + t); }
   __device__ uint32_t fin(int t) const { return base + 8 * (1 + 5 * S + 4 * nq + t); }
+  __device__ uint32_t turn(int t, int quarter) const { return base + 8 * (1 + 5 * S + 5 * nq + 4 * t + quarter); }
 };
 
 // The key tiles of one query tile (or of all): [first, last), and which of them need masks.
@@ -170,18 +174,36 @@ struct Bounds {
   __device__ bool whole(int j) const { return j * BN >= lo_last && (j + 1) * BN <= hi_first; }
 };
 
+// One lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 
-// exp2_poly2 with an exact zero below 2^-125: a masked key's probability must not be merely small.
+// 2^x for two values on the FMA pipe like exp2_poly2 (the same reduction and polynomial), with an
+// exact zero for x = -infinity: a masked key's probability must not be merely small. The exponent is
+// added and kept from going negative in one instruction.
 __device__ __forceinline__ void exp2_poly2_zero(float& y0, float& y1, float x0, float x1) {
-  float a, b;
-  exp2_poly2(a, b, x0, x1);
-  y0 = x0 < -125.0f ? 0.f : a;
-  y1 = x1 < -125.0f ? 0.f : b;
+  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it leaves round(x) in the low mantissa bits
+  constexpr float c0 = 9.999280572e-01f, c1 = 6.932609677e-01f, c2 = 2.426111251e-01f, c3 = 5.517166853e-02f;
+  x0 = fmaxf(x0, -200.0f);
+  x1 = fmaxf(x1, -200.0f);
+  float t0, t1, n0, n1, f0, f1, p0, p1;
+  add2(t0, t1, x0, x1, kRound, kRound);
+  sub2(n0, n1, t0, t1, kRound, kRound);
+  sub2(f0, f1, x0, x1, n0, n1);
+  fma2(p0, p1, c3, c3, f0, f1, c2, c2);
+  fma2(p0, p1, p0, p1, f0, f1, c1, c1);
+  fma2(p0, p1, p0, p1, f0, f1, c0, c0);
+  y0 = __int_as_float(__viaddmax_s32(__float_as_int(p0), __float_as_int(t0) << 23, 0));
+  y1 = __int_as_float(__viaddmax_s32(__float_as_int(p1), __float_as_int(t1) << 23, 0));
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -246,6 +268,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(bars.p_full(t), 128);
       mbar_init(bars.o_done(t), 1);
       mbar_init(bars.fin(t), 1);
+      for (int i = 0; i < 4; ++i) mbar_init(bars.turn(t, i), 1);
     }
     *abort_flag = 0;
     *cleaned = 0;
@@ -335,65 +358,78 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       __syncwarp();
     } else if (warp <= NQ) {
       // ---------------------------------------------------------------- MMA issuer of query tile t
-      const int t = warp - 1;
-      if (lane == 0) {
+      // The whole warp runs the loop and one elected lane issues: descriptors then live in uniform
+      // registers (a lane of its own spent 100 to 175 cycles on every MMA).
+      auto issuer = [&](auto tile) {
+        constexpr int t = decltype(tile)::value;
         const int ksteps = (p.dh + 15) / 16;
         constexpr uint32_t idesc_qk = idesc_f16kind_f32(BM, BN, false, C::F16);
         const uint32_t idesc_pv = idesc_f16kind_f32(BM, 16, true, C::F16) + (static_cast<uint32_t>((ksteps * 16 - 16) >> 3) << 17);
         const uint32_t tS = tmem + t * C::TM_TILE, tP = tS + C::TM_P, tO = tS + C::TM_O;
-        const uint32_t tq = sbase + t * C::Q_TILE;
+        // Descriptors count addresses in units of 16 bytes.
+        const uint64_t q_desc = smem_desc(sbase + t * C::Q_TILE, 16, 1024), k_desc = smem_desc(sbase + C::K_OFF, 16, 1024);
+        const uint64_t v_desc = smem_desc(sbase + C::V_OFF, BN * 128, 1024);
+        const Bounds mine = tb[t];
+        auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, p.err)) != 0; };
         auto issue_qk = [&](int s) {
-          for (int ks = 0; ks < ksteps; ++ks) {
-            const uint64_t a = smem_desc(tq + (ks >> 2) * (BM * 128) + (ks & 3) * 32, 16, 1024);
-            const uint64_t bd = smem_desc(sbase + C::K_OFF + s * C::KV_TILE + (ks >> 2) * (BN * 128) + (ks & 3) * 32, 16, 1024);
-            mma_ss(tS, a, bd, idesc_qk, ks > 0 ? 1u : 0u);
+          const uint64_t kd = k_desc + static_cast<uint32_t>(s * (C::KV_TILE / 16));
+          if (elect_one()) {
+#pragma unroll
+            for (int ks = 0; ks < C::DHT / 16; ++ks)
+              if (ks < ksteps)
+                mma_ss(tS, q_desc + (ks >> 2) * (BM * 8) + (ks & 3) * 2, kd + (ks >> 2) * (BN * 8) + (ks & 3) * 2, idesc_qk,
+                       ks > 0 ? 1u : 0u);
+            mma_commit(bars.s_full(t));
           }
-          mma_commit(bars.s_full(t));
+          __syncwarp();
         };
         auto issue_pv = [&](int s, bool first) {
+          const uint64_t vd = v_desc + static_cast<uint32_t>(s * (C::KV_TILE / 16));
+          if (elect_one()) {
 #pragma unroll
-          for (int ks = 0; ks < BN / 16; ++ks) {
-            const uint64_t bd = smem_desc(sbase + C::V_OFF + s * C::KV_TILE + ks * 16 * 128, BN * 128, 1024);
-            mma_ts(tO, tP + ks * 8, bd, idesc_pv, (!first || ks > 0) ? 1u : 0u);
+            for (int ks = 0; ks < BN / 16; ++ks) mma_ts(tO, tP + ks * 8, vd + ks * 128, idesc_pv, (!first || ks > 0) ? 1u : 0u);
+            mma_commit(bars.o_done(t));
+            mma_commit(bars.kv_empty(s));
           }
-          mma_commit(bars.o_done(t));
-          mma_commit(bars.kv_empty(s));
+          __syncwarp();
         };
         // S of the next tile is issued before P V of this one, as soon as S has been read; where P lies
         // over S, once P V is complete. Key tiles that this query tile does not need are released as
         // they arrive, after the P V that is still to come: its own stage must not wait for them.
-        bool ok = j1 <= j0 || wait_bar(bars.q_full(), 0, abort_flag, p.err);
-        int n = 0, pending = -1;  // S issued so far; ring position of the tile whose P V is still to come
+        bool ok = j1 <= j0 || wait(bars.q_full(), 0);
+        int n = 0, pending = -1, pending_parity = 0;  // S issued so far; stage of the tile whose P V is still to come
         auto finish = [&] {
           if (pending < 0) return true;
-          if (!wait_bar(bars.p_full(t), (n - 1) & 1, abort_flag, p.err)) return false;
-          if (!wait_bar(bars.v_ready(pending % STAGES), (pending / STAGES) & 1, abort_flag, p.err)) return false;
+          if (!wait(bars.p_full(t), (n - 1) & 1) || !wait(bars.v_ready(pending), pending_parity)) return false;
           tc_fence_after();
-          issue_pv(pending % STAGES, n == 1);
+          issue_pv(pending, n == 1);
           pending = -1;
           return true;
         };
-        for (int j = j0, g = 0; ok && j < j1; ++j, ++g) {
-          const int s = g % STAGES;
-          const bool held = tb[t].template holds<BN>(j);
+        int s = 0, parity = 0;  // ring position
+        for (int j = j0; ok && j < j1; ++j) {
+          const bool held = mine.template holds<BN>(j);
           if ((!held || !C::P_SEP) && !(ok = finish())) break;
-          if (!(ok = wait_bar(bars.k_full(s), (g / STAGES) & 1, abort_flag, p.err))) break;
+          if (!(ok = wait(bars.k_full(s), parity))) break;
           if (!held) {
-            mbar_arrive(bars.kv_empty(s));
-            continue;
+            if (lane == 0) mbar_arrive(bars.kv_empty(s));
+          } else {
+            if (n > 0 && !(ok = wait(C::P_SEP ? bars.s_free(t) : bars.o_done(t), (n - 1) & 1))) break;
+            tc_fence_after();
+            issue_qk(s);
+            if (C::P_SEP && !(ok = finish())) break;  // (its counts are those before this S)
+            ++n;
+            pending = s;
+            pending_parity = parity;
           }
-          if (n > 0 && !(ok = wait_bar(C::P_SEP ? bars.s_free(t) : bars.o_done(t), (n - 1) & 1, abort_flag, p.err))) break;
-          tc_fence_after();
-          issue_qk(s);
-          // (P_SEP) the counts of finish() are those before this S
-          if (C::P_SEP && !(ok = finish())) break;
-          ++n;
-          pending = g;
+          if (++s == STAGES) s = 0, parity ^= 1;
         }
         if (ok) finish();
-        mma_commit(bars.fin(t));
+        if (elect_one()) mma_commit(bars.fin(t));
         wait_bar(bars.fin(t), 0, abort_flag, p.err, false);
-      }
+      };
+      if (warp == 1) issuer(std::integral_constant<int, 0>());
+      else if constexpr (NQ == 2) issuer(std::integral_constant<int, 1>());
       __syncwarp();
     } else if (warp == 3) {
       // ---------------------------------------------------------------- guard
@@ -448,41 +484,58 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   } else {
     // ================================================================== softmax warpgroups
     if constexpr (NQ == 2) regs_inc<C::REG_SOFT>();
-    const int t = r_in / BM, quarter = warp & 3;
+    const int t = NQ == 1 ? 0 : warp >> 3, quarter = warp & 3;
     const uint32_t tbase = tmem + t * C::TM_TILE + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t tS = tbase, tP = tbase + C::TM_P, tO = tbase + C::TM_O;
-    Bounds mine = tb[0];
-    if (NQ == 2 && t == 1) mine = tb[NQ - 1];
-    const long long row = row0 + r_in;
+    const Bounds mine = NQ == 2 && t == 1 ? tb[NQ - 1] : tb[0];
     const bool live = row0 + (r_in & ~31) < rows;  // a warp behind the last row only keeps the barriers going
     const bool is_mixed = C::BIAS && *mixed;
     const int ochunks = (p.dh + 15) / 16;
+    // This tile's key tiles, [jf, jl) of the CTA's; element masks outside [wf, wl).
+    const int jf = max(j0, mine.template first<BN>()), jl = mine.empty() ? jf : min(j1, mine.template last<BN>());
+    const int wf = (mine.lo_last + BN - 1) / BN, wl = mine.hi_first / BN;
+    // Turns: where both query tiles need a key tile, their warps on one SM sub-partition take its
+    // special-function unit one after the other (tile 0 first), so that one tile's exp2 phase overlaps
+    // the other's maxima, loads, stores and MMAs. Tile t waits for turn(t), and passes the turn on.
+    int both0 = 0, both1 = 0;
+    if (NQ == 2 && !tb[0].empty() && !tb[NQ - 1].empty()) {
+      both0 = max(tb[0].template first<BN>(), tb[NQ - 1].template first<BN>());
+      both1 = min(tb[0].template last<BN>(), tb[NQ - 1].template last<BN>());
+    }
+    auto take_turn = [&](int j) {
+      if (t == 0 && j == both0) return true;
+      return __all_sync(0xffffffffu, wait_bar(bars.turn(t, quarter), (t == 0 ? j - both0 - 1 : j - both0) & 1, abort_flag, p.err)) != 0;
+    };
+    auto pass_turn = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars.turn(1 - t, quarter));
+    };
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
-    int n = 0;
-    for (int j = j0, g = 0; j < j1; ++j, ++g) {
-      if (!mine.template holds<BN>(j)) continue;
-      if (!__all_sync(0xffffffffu, wait_bar(bars.s_full(t), n & 1, abort_flag, p.err))) {
+    if (!live) {
+      for (int j = jf; ok && j < jl; ++j) {
+        const int par = (j - jf) & 1;
+        ok = __all_sync(0xffffffffu, wait_bar(bars.s_full(t), par, abort_flag, p.err));
+        if (ok && C::P_SEP) mbar_arrive(bars.s_free(t));
+        // as the other warps: no arrival for this P before every warp's for the one before it
+        if (ok && j > jf) ok = __all_sync(0xffffffffu, wait_bar(bars.o_done(t), par ^ 1, abort_flag, p.err));
+        if (ok) mbar_arrive(bars.p_full(t));
+        if (NQ == 2 && ok && j >= both0 && j < both1) {
+          ok = take_turn(j);
+          if (ok) pass_turn();
+        }
+      }
+    }
+    for (int j = jf; live && j < jl; ++j) {
+      if (!__all_sync(0xffffffffu, wait_bar(bars.s_full(t), (j - jf) & 1, abort_flag, p.err))) {
         ok = false;
         break;
       }
-      if (C::BIAS && !__all_sync(0xffffffffu, wait_bar(bars.bias_full(g % STAGES), (g / STAGES) & 1, abort_flag, p.err))) {
+      if (C::BIAS && !__all_sync(0xffffffffu, wait_bar(bars.bias_full((j - j0) % STAGES), ((j - j0) / STAGES) & 1, abort_flag, p.err))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      if (!live) {
-        tc_fence_before();
-        if (C::P_SEP) mbar_arrive(bars.s_free(t));
-        // as the other warps: no arrival for this P before every warp's for the one before it
-        if (n > 0 && !__all_sync(0xffffffffu, wait_bar(bars.o_done(t), (n - 1) & 1, abort_flag, p.err))) {
-          ok = false;
-          break;
-        }
-        mbar_arrive(bars.p_full(t));
-        ++n;
-        continue;
-      }
       float sv[BN];
 #pragma unroll
       for (int c = 0; c < BN / 32; ++c) {
@@ -504,12 +557,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
       if constexpr (C::BIAS) {
         if (!is_mixed) {
-          const float* w = reinterpret_cast<const float*>(smem + C::BIAS_OFF) + (g % STAGES) * C::WINDOW + (NQ * BM - 1 - r_in);
+          const float* w = reinterpret_cast<const float*>(smem + C::BIAS_OFF) + ((j - j0) % STAGES) * C::WINDOW + (NQ * BM - 1 - r_in);
 #pragma unroll
           for (int i = 0; i < BN; ++i) sv[i] = C::CAP ? sv[i] + w[i] : fmaf(sv[i], p.scale_log2, w[i]);
         } else {  // a tile over documents with different shifts: each row its own distances
           const float* table = p.bias + static_cast<long long>(h0) * (2LL * p.radius + 1) + p.radius;
-          const long long d0 = static_cast<long long>(j) * BN - row / p.pack + me.shift;
+          const long long d0 = static_cast<long long>(j) * BN - (row0 + r_in) / p.pack + me.shift;
 #pragma unroll
           for (int i = 0; i < BN; ++i) {
             const float x = __ldg(table + clampll(d0 + i, -p.radius, p.radius));
@@ -519,7 +572,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           }
         }
       }
-      if (!mine.template whole<BN>(j)) {
+      if (__builtin_expect(j < wf || j >= wl, 0)) {
         const int lo = me.lo - j * BN, hi = me.hi - j * BN;
 #pragma unroll
         for (int i = 0; i < BN; ++i)
@@ -542,10 +595,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const float alpha = !raise ? 1.0f : m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
       if (raise) m_run = m_new;
       const float neg_m = m_run == -INFINITY ? 0.f : -m_run;  // a row that has seen nothing: all its exp2 are 0
+      const bool turns = NQ == 2 && j >= both0 && j < both1;
+      if (turns && !take_turn(j)) {
+        ok = false;
+        break;
+      }
       uint32_t pk[BN / 2];
       float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
 #pragma unroll
       for (int i = 0; i < BN / 2; ++i) {
+        if (i == C::PASS && turns) pass_turn();
         float x0, x1;
         if constexpr (kLog2) add2(x0, x1, sv[2 * i], sv[2 * i + 1], neg_m, neg_m);
         else fma2(x0, x1, sv[2 * i], sv[2 * i + 1], p.scale_log2, p.scale_log2, neg_m, neg_m);
@@ -560,8 +619,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         pk[i] = C::F16 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
       }
       l_run = fmaf(l_run, alpha, (ls0 + ls1) + (ls2 + ls3));
-      if (n > 0) {
-        if (!__all_sync(0xffffffffu, wait_bar(bars.o_done(t), (n - 1) & 1, abort_flag, p.err))) {
+      if (j > jf) {
+        if (!__all_sync(0xffffffffu, wait_bar(bars.o_done(t), (j - jf - 1) & 1, abort_flag, p.err))) {
           ok = false;
           break;
         }
@@ -587,11 +646,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(bars.p_full(t));
-      ++n;
     }
-    if (ok && n > 0) ok = __all_sync(0xffffffffu, wait_bar(bars.o_done(t), (n - 1) & 1, abort_flag, p.err));
+    if (ok && jl > jf) ok = __all_sync(0xffffffffu, wait_bar(bars.o_done(t), (jl - jf - 1) & 1, abort_flag, p.err));
     tc_fence_after();
     // ------------------------------------------------------------------ epilogue, one row a thread
+    const long long row = row0 + r_in;
     const int i_q = static_cast<int>(row / p.pack), h = h0 + static_cast<int>(row % p.pack);
     // Values that the guard set to zero, for rows that see them: 16 columns from c16 of the masked tiles.
     auto add_cleaned = [&](int c16, float (&o)[16]) {
@@ -614,7 +673,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
     };
-    const bool has_o = n > 0 && ok, fix = has_o && *cleaned;  // the same for the warp
+    const bool has_o = jl > jf && ok, fix = has_o && *cleaned;  // the same for the warp
     const bool join = NQ == 1 && splits > 1;
     const bool store = row < rows && (join || (me.exists && ok));
     // A part of a cluster's join goes over the ring: its copies and MMAs are done with the last P V.
