@@ -28,6 +28,8 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -54,7 +56,8 @@ struct Params {
   int heads, group;      // query heads; query heads per key head
   int pack;              // heads that are rows of one tile (1 or group)
   int Lq, Lk, dh, docs, radius, causal;
-  int tiles;             // CTAs (clusters) per (batch, packed head)
+  int tiles;             // query tiles of a plane (one batch's packed head)
+  int planes, plane_group;  // planes; planes whose items are mixed
   float scale_log2;      // scale * log2(e)
   float cap_in, cap_out; // 2 log2(e) scale / cap, cap log2(e)
   unsigned int* err;
@@ -111,74 +114,116 @@ __device__ inline Row row_of(const Params& p, int b, int i) {
   return r;
 }
 
-// DHT: padded head size (64-column chunks of shared memory; N of O is dh rounded up to 16).
-template <int DHT_, int BN_, int NQ_, int STAGES_, bool P_SEP_, bool F16_, bool CAP_, bool BIAS_>
+// DHT: padded head size (64-column chunks of shared memory; N of O is dh rounded up to 16). BN: keys of
+// a tile. KS, VS: stages of the rings of key and value tiles. CTAS: CTAs of an SM.
+template <int DHT_, int BN_, int KS_, int VS_, int CTAS_, bool P_SEP_, bool F16_, bool CAP_, bool BIAS_>
 struct Cfg {
-  static constexpr int DHT = DHT_, BN = BN_, NQ = NQ_, STAGES = STAGES_;
+  static constexpr int DHT = DHT_, BN = BN_, KS = KS_, VS = VS_, CTAS = CTAS_;
   static constexpr bool P_SEP = P_SEP_, F16 = F16_, CAP = CAP_, BIAS = BIAS_;
+#ifndef HV
+#define HV 1
+#endif
+  static constexpr int HALVES = HV;        // threads that share a row
+  static constexpr int HC = BN / HALVES;   // columns of a softmax thread
   static constexpr int NCH = (DHT + 63) / 64;
   static constexpr int Q_TILE = NCH * BM * 128, KV_TILE = NCH * BN * 128;
-  static constexpr int K_OFF = NQ * Q_TILE, V_OFF = K_OFF + STAGES * KV_TILE;
-  static constexpr int BIAS_OFF = V_OFF + STAGES * KV_TILE;
-  static constexpr int WINDOW = NQ * BM + BN;  // values of one bias window (one unused)
-  static constexpr int BAR_OFF = BIAS_OFF + (BIAS ? STAGES * WINDOW * 4 : 0);
-  // q_full, k_full[S], v_full[S], v_ready[S], kv_empty[S], bias_full[S], s_full, s_free, p_full, o_done, fin [NQ],
-  // turn[NQ][4]
-  static constexpr int NBARS = 1 + 5 * STAGES + 9 * NQ;
+  static constexpr int K_OFF = Q_TILE, V_OFF = K_OFF + KS * KV_TILE;
+  static constexpr int BIAS_OFF = V_OFF + VS * KV_TILE;
+  static constexpr int WINDOW = BM + BN;  // values of one bias window (one unused); one for each stage of V
+  // The two halves of a row exchange their maxima (two buffers) and, at the end, their sums.
+  static constexpr int XCH_OFF = BIAS_OFF + (BIAS ? VS * WINDOW * 4 : 0);
+  static constexpr int BAR_OFF = XCH_OFF + (HALVES == 2 ? 2 * 2 * BM * 4 : 0);
+  // q_full, s_full, s_free, p_full, o_done, fin, halves[4], k_full[KS], k_empty[KS], v_full[VS], v_ready[VS],
+  // v_empty[VS], bias_full[VS]
+  static constexpr int NBARS = 10 + 2 * KS + 4 * VS;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // TMEM address, abort flag, cleaned flag, mixed flag
-  static constexpr int BOUNDS_OFF = MISC_OFF + 16;      // per query tile: lo of its first and last row, hi of both
-  static constexpr int SMEM = BOUNDS_OFF + NQ * 16 + 1024;
+  static constexpr int BOUNDS_OFF = MISC_OFF + 16;      // lo of the first and last row, hi of both
+  static constexpr int SMEM = BOUNDS_OFF + 16;
   static constexpr int TM_P = P_SEP ? BN : 0, TM_O = P_SEP ? BN + BN / 2 : BN;
-  static constexpr int TM_TILE = TM_O + DHT <= 256 ? 256 : 512;
-  static constexpr int TM_COLS = NQ * TM_TILE;
-  static constexpr int THREADS = 128 + 128 * NQ;
-  static constexpr int REG_HELPER = 120, REG_SOFT = 192;
+  static constexpr int TM_COLS = TM_O + DHT <= 256 ? 256 : 512;
+  static constexpr int THREADS = 128 + 128 * HALVES;
+#ifndef RH
+#define RH 64
+#define RS 192
+#endif
+  static constexpr int REG_HELPER = RH, REG_SOFT = RS;  // two CTAs an SM: registers move to the softmax warps
   // Of every 8 column pairs this many take exp2 on the FMA pipe; with a cap or bias that pipe has other work.
-  static constexpr int POLY = CAP || BIAS ? 0 : 2;
-  static constexpr int PASS = BN / 4;  // column pairs (of BN / 2) after which a warp passes its turn on
-  // Join of a cluster's parts: rows of DHT fp32 and (m, l), over the K/V ring.
+#ifndef NPOLY
+#define NPOLY 2
+#endif
+  static constexpr int POLY = CAP || BIAS ? 0 : NPOLY;
+  // Join of a cluster's parts: rows of DHT fp32 and (m, l), over Q and the rings.
   static constexpr int JOIN_ROW = DHT + 4;  // floats a row (+4: rows start in different banks)
-  static_assert(TM_COLS <= 512 && SMEM <= 227 * 1024, "on-chip memory");
-  static_assert(NQ != 1 || BM * JOIN_ROW * 4 <= 2 * STAGES * KV_TILE, "the join fits the ring");
-  static_assert(NQ != 2 || 128 * REG_HELPER + 256 * REG_SOFT <= 168 * 384, "register split");
+  static_assert(CTAS * TM_COLS <= 512 && CTAS * (SMEM + 1024) <= 228 * 1024, "on-chip memory");
+  static_assert(BM * JOIN_ROW * 4 <= Q_TILE + (KS + VS) * KV_TILE, "the join fits Q and the rings");
 };
 
+template <int KS, int VS>
 struct Bars {
   uint32_t base;
-  int S, nq;
   __device__ uint32_t q_full() const { return base; }
-  __device__ uint32_t k_full(int s) const { return base + 8 * (1 + s); }
-  __device__ uint32_t v_full(int s) const { return base + 8 * (1 + S + s); }
-  __device__ uint32_t v_ready(int s) const { return base + 8 * (1 + 2 * S + s); }
-  __device__ uint32_t kv_empty(int s) const { return base + 8 * (1 + 3 * S + s); }
-  __device__ uint32_t bias_full(int s) const { return base + 8 * (1 + 4 * S + s); }
-  __device__ uint32_t s_full(int t) const { return base + 8 * (1 + 5 * S + t); }
-  __device__ uint32_t s_free(int t) const { return base + 8 * (1 + 5 * S + nq + t); }
-  __device__ uint32_t p_full(int t) const { return base + 8 * (1 + 5 * S + 2 * nq + t); }
-  __device__ uint32_t o_done(int t) const { return base + 8 * (1 + 5 * S + 3 * nq + t); }
-  __device__ uint32_t fin(int t) const { return base + 8 * (1 + 5 * S + 4 * nq + t); }
-  __device__ uint32_t turn(int t, int quarter) const { return base + 8 * (1 + 5 * S + 5 * nq + 4 * t + quarter); }
+  __device__ uint32_t s_full() const { return base + 8; }
+  __device__ uint32_t s_free() const { return base + 16; }
+  __device__ uint32_t p_full() const { return base + 24; }
+  __device__ uint32_t o_done() const { return base + 32; }
+  __device__ uint32_t fin() const { return base + 40; }
+  __device__ uint32_t halves(int quarter) const { return base + 48 + 8 * quarter; }
+  __device__ uint32_t k_full(int s) const { return base + 8 * (10 + s); }
+  __device__ uint32_t k_empty(int s) const { return base + 8 * (10 + KS + s); }
+  __device__ uint32_t v_full(int s) const { return base + 8 * (10 + 2 * KS + s); }
+  __device__ uint32_t v_ready(int s) const { return base + 8 * (10 + 2 * KS + VS + s); }
+  __device__ uint32_t v_empty(int s) const { return base + 8 * (10 + 2 * KS + 2 * VS + s); }
+  __device__ uint32_t bias_full(int s) const { return base + 8 * (10 + 2 * KS + 3 * VS + s); }
 };
 
-// The key tiles of one query tile (or of all): [first, last), and which of them need masks.
+// A position in a ring of N stages, and the parity of its phase.
+template <int N>
+struct Ring {
+  int s = 0, parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == N) s = 0, parity ^= 1;
+  }
+};
+
+// The keys that the first and last row of a query tile see.
 struct Bounds {
   int lo_first, lo_last, hi_first, hi_last;
-  __device__ bool empty() const { return hi_last <= lo_first; }
-  template <int BN>
-  __device__ int first() const { return lo_first / BN; }
-  template <int BN>
-  __device__ int last() const { return (hi_last + BN - 1) / BN; }
-  template <int BN>
-  __device__ bool holds(int j) const { return !empty() && j >= first<BN>() && j < last<BN>(); }
-  template <int BN>
-  __device__ bool whole(int j) const { return j * BN >= lo_last && (j + 1) * BN <= hi_first; }
 };
+
+// Whether a lane's share of n packs of 16-bit values holds no infinity and no NaN: each value times
+// zero is zero, or NaN. Eight packs are in flight at a time (n is a multiple of 256).
+template <bool F16>
+__device__ __forceinline__ bool all_finite(const uint4* tile, int n, int lane) {
+  using T2 = std::conditional_t<F16, __half2, __nv_bfloat162>;
+  const uint32_t zero_bits = 0;
+  const T2 zero = *reinterpret_cast<const T2*>(&zero_bits);
+  T2 acc[4] = {zero, zero, zero, zero};
+  for (int i = lane; i < n; i += 256) {
+    uint4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = tile[i + 32 * k];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const T2* v = reinterpret_cast<const T2*>(&x[k]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = __hfma2(v[e], zero, acc[e]);
+    }
+  }
+  const T2 sum = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+  return __heq2(sum, sum).x != static_cast<decltype(sum.x)>(0.f) && __heq2(sum, sum).y != static_cast<decltype(sum.x)>(0.f);
+}
 
 // One lane of a converged warp, always the same one.
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(one));
   return one != 0;
+}
+
+// A bias in units of log2; the lowest finite value stays finite.
+__device__ __forceinline__ float bias_log2(float x) {
+  const float y = x * 1.4426950408889634f;
+  return isinf(y) && !isinf(x) ? copysignf(3.402823466e38f, x) : y;
 }
 
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -228,14 +273,13 @@ __device__ __forceinline__ float4 peer_load4(uint32_t addr, uint32_t rank) {
 }
 
 template <class C>
-__global__ void __launch_bounds__(C::THREADS, 1)
+__global__ void __launch_bounds__(C::THREADS, C::CTAS)
     attention_masked_sm100(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
-  constexpr int BN = C::BN, NQ = C::NQ, STAGES = C::STAGES;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int BN = C::BN, KS = C::KS, VS = C::VS, HALVES = C::HALVES;
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's period
   const uint32_t sbase = smem_u32(smem);
-  const Bars bars{sbase + C::BAR_OFF, STAGES, NQ};
+  const Bars<KS, VS> bars{sbase + C::BAR_OFF};
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 4);
   volatile int* cleaned = reinterpret_cast<volatile int*>(smem + C::MISC_OFF + 8);  // the guard set a value to zero
@@ -243,37 +287,39 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   Bounds* bounds = reinterpret_cast<Bounds*>(smem + C::BOUNDS_OFF);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int splits = NQ == 1 ? static_cast<int>(cluster_size()) : 1;
-  const int rank = NQ == 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int item = blockIdx.x / splits;
-  // Late queries first: with a causal mask they see the most keys.
-  const int qt = p.tiles - 1 - item % p.tiles;
+  const int splits = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  // Items in groups of planes (a plane is one batch's packed heads), within a group the late queries
+  // first: with a causal mask they see the most keys, and short items at the end even out the SMs.
+  const int item = blockIdx.x / splits, planes = p.planes;
+  const int group0 = item / (p.plane_group * p.tiles) * p.plane_group, group_n = min(p.plane_group, planes - group0);
+  const int in_group = item - group0 * p.tiles;
+  const int qt = p.tiles - 1 - in_group / group_n, plane = group0 + in_group % group_n;
   const int heads_packed = p.heads / p.pack;
-  const int bh = item / p.tiles, b = bh / heads_packed, h0 = bh % heads_packed * p.pack, kvh = h0 / p.group;
+  const int b = plane / heads_packed, h0 = plane % heads_packed * p.pack, kvh = h0 / p.group;
   const long long rows = static_cast<long long>(p.Lq) * p.pack;    // of this (batch, packed head)
-  const long long row0 = static_cast<long long>(qt) * (NQ * BM);
+  const long long row0 = static_cast<long long>(qt) * BM;
 
   if (threadIdx.x == 0) {
     mbar_init(bars.q_full(), 1);
-    for (int s = 0; s < STAGES; ++s) {
+    mbar_init(bars.s_full(), 1);
+    mbar_init(bars.s_free(), 128 * HALVES);
+    mbar_init(bars.p_full(), 128 * HALVES);
+    mbar_init(bars.o_done(), 1);
+    mbar_init(bars.fin(), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(bars.halves(i), 2);
+    for (int s = 0; s < KS; ++s) {
       mbar_init(bars.k_full(s), 1);
+      mbar_init(bars.k_empty(s), 1);
+    }
+    for (int s = 0; s < VS; ++s) {
       mbar_init(bars.v_full(s), 1);
       mbar_init(bars.v_ready(s), 1);
-      mbar_init(bars.kv_empty(s), NQ);
+      mbar_init(bars.v_empty(s), 1);
       mbar_init(bars.bias_full(s), 1);
-    }
-    for (int t = 0; t < NQ; ++t) {
-      mbar_init(bars.s_full(t), 1);
-      mbar_init(bars.s_free(t), 128);
-      mbar_init(bars.p_full(t), 128);
-      mbar_init(bars.o_done(t), 1);
-      mbar_init(bars.fin(t), 1);
-      for (int i = 0; i < 4; ++i) mbar_init(bars.turn(t, i), 1);
     }
     *abort_flag = 0;
     *cleaned = 0;
     *mixed = 0;
-    for (int t = 0; t < NQ; ++t) bounds[t] = Bounds{0, 0, 0, 0};
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -285,260 +331,223 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
+  sd::grid_dep_wait();  // global memory from here on
+  sd::grid_dep_launch();
+
+  // Softmax threads: half of the columns (warps 4-7 the first), row of the tile.
+  const int half = HALVES == 2 ? warp >> 3 : 0, r_in = (warp & 3) * 32 + lane;
+  Row me{0, 0, 0, false};
+  if (warp >= 4) {
+    const long long r = row0 + r_in;
+    if (r < rows) {
+      me = row_of(p, b, static_cast<int>(r / p.pack));
+      if (r_in == 0) bounds->lo_first = me.lo, bounds->hi_first = me.hi;
+      if (r_in == BM - 1 || r == rows - 1) bounds->lo_last = me.lo, bounds->hi_last = me.hi;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  sd::grid_dep_wait();  // global memory from here on
-  sd::grid_dep_launch();
-
-  Row me{0, 0, 0, false};
-  const int r_in = static_cast<int>(threadIdx.x) - 128;  // row within the CTA (softmax threads)
-  if (r_in >= 0) {
-    const long long r = row0 + r_in;
-    if (r < rows) {
-      me = row_of(p, b, static_cast<int>(r / p.pack));
-      const int t = r_in / BM;
-      if (r_in % BM == 0) bounds[t].lo_first = me.lo, bounds[t].hi_first = me.hi;
-      if (r_in % BM == BM - 1 || r == rows - 1) bounds[t].lo_last = me.lo, bounds[t].hi_last = me.hi;
-    }
-  }
-  __syncthreads();
   long long shift0 = 0;
   if constexpr (C::BIAS) {
-    // The window of distances assumes one shift for the CTA's rows; documents may differ in theirs.
+    // The window of distances assumes one shift for the tile's rows; documents may differ in theirs.
     shift0 = row_of(p, b, static_cast<int>(row0 / p.pack)).shift;
     if (me.exists && me.hi > me.lo && me.shift != shift0) *mixed = 1;
     __syncthreads();
   }
-  Bounds tb[NQ];
-#pragma unroll
-  for (int t = 0; t < NQ; ++t) tb[t] = bounds[t];
-  int j0 = 0x7fffffff, j1 = 0;
-#pragma unroll
-  for (int t = 0; t < NQ; ++t)
-    if (!tb[t].empty()) j0 = min(j0, tb[t].template first<BN>()), j1 = max(j1, tb[t].template last<BN>());
-  if (j1 <= j0) j0 = j1 = 0;
-  if (NQ == 1 && splits > 1) {  // this CTA's part of the key tiles
+  // Key tiles [j0, j1) of this CTA; those outside [whole0, whole1) need element masks.
+  const Bounds tb = *bounds;
+  int j0 = tb.lo_first / BN, j1 = tb.hi_last > tb.lo_first ? (tb.hi_last + BN - 1) / BN : j0;
+  const int whole0 = (tb.lo_last + BN - 1) / BN, whole1 = tb.hi_first / BN;
+  if (splits > 1) {
     const long long n = j1 - j0;
     const int a = j0 + static_cast<int>(n * rank / splits), e = j0 + static_cast<int>(n * (rank + 1) / splits);
     j0 = a, j1 = e;
   }
 
   if (warp < 4) {
-    // ================================================================== helper warpgroup
-    if constexpr (NQ == 2) regs_dec<C::REG_HELPER>();
+    // ================================================================== helper warps
+    if constexpr (C::CTAS == 2) regs_dec<C::REG_HELPER>();
     const int chunks = (p.dh + 63) / 64;
     if (warp == 0) {
       // ---------------------------------------------------------------- TMA producer
       if (lane == 0 && j1 > j0) {
-        mbar_arrive_expect_tx(bars.q_full(), NQ * chunks * BM * 128);
-        for (int t = 0; t < NQ; ++t)
+        mbar_arrive_expect_tx(bars.q_full(), chunks * BM * 128);
+        for (int c = 0; c < chunks; ++c)
+          tma_load_4d(sbase + c * BM * 128, &tm_q, bars.q_full(), c * 64, h0, static_cast<int>(row0 / p.pack), b);
+        Ring<KS> rk;
+        Ring<VS> rv;
+        int nk = 0, nv = 0;  // tiles issued
+        for (int j = j0; j < j1; ++j) {
+          if (nk >= KS && !wait_bar(bars.k_empty(rk.s), rk.parity ^ 1, abort_flag, p.err)) break;
+          mbar_arrive_expect_tx(bars.k_full(rk.s), chunks * BN * 128);
           for (int c = 0; c < chunks; ++c)
-            tma_load_4d(sbase + t * C::Q_TILE + c * BM * 128, &tm_q, bars.q_full(), c * 64, h0,
-                        static_cast<int>((row0 + t * BM) / p.pack), b);
-        int g = 0;
-        for (int j = j0; j < j1; ++j, ++g) {
-          const int s = g % STAGES;
-          if (g >= STAGES && !wait_bar(bars.kv_empty(s), (g / STAGES - 1) & 1, abort_flag, p.err)) break;
-          mbar_arrive_expect_tx(bars.k_full(s), chunks * BN * 128);
+            tma_load_4d(sbase + C::K_OFF + rk.s * C::KV_TILE + c * BN * 128, &tm_k, bars.k_full(rk.s), c * 64, kvh, j * BN, b);
+          ++nk;
+          rk.next();
+          if (nv >= VS && !wait_bar(bars.v_empty(rv.s), rv.parity ^ 1, abort_flag, p.err)) break;
+          mbar_arrive_expect_tx(bars.v_full(rv.s), chunks * BN * 128);
           for (int c = 0; c < chunks; ++c)
-            tma_load_4d(sbase + C::K_OFF + s * C::KV_TILE + c * BN * 128, &tm_k, bars.k_full(s), c * 64, kvh, j * BN, b);
-          mbar_arrive_expect_tx(bars.v_full(s), chunks * BN * 128);
-          for (int c = 0; c < chunks; ++c)
-            tma_load_4d(sbase + C::V_OFF + s * C::KV_TILE + c * BN * 128, &tm_v, bars.v_full(s), c * 64, kvh, j * BN, b);
+            tma_load_4d(sbase + C::V_OFF + rv.s * C::KV_TILE + c * BN * 128, &tm_v, bars.v_full(rv.s), c * 64, kvh, j * BN, b);
+          ++nv;
+          rv.next();
         }
         // Every copy has landed before the CTA may exit.
         wait_bar(bars.q_full(), 0, abort_flag, p.err, false);
-        for (int k = max(0, g - STAGES); k < g; ++k) {
-          wait_bar(bars.k_full(k % STAGES), (k / STAGES) & 1, abort_flag, p.err, false);
-          wait_bar(bars.v_full(k % STAGES), (k / STAGES) & 1, abort_flag, p.err, false);
-        }
+        for (int k = max(0, nk - KS); k < nk; ++k) wait_bar(bars.k_full(k % KS), (k / KS) & 1, abort_flag, p.err, false);
+        for (int k = max(0, nv - VS); k < nv; ++k) wait_bar(bars.v_full(k % VS), (k / VS) & 1, abort_flag, p.err, false);
       }
       __syncwarp();
-    } else if (warp <= NQ) {
-      // ---------------------------------------------------------------- MMA issuer of query tile t
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issuer
       // The whole warp runs the loop and one elected lane issues: descriptors then live in uniform
       // registers (a lane of its own spent 100 to 175 cycles on every MMA).
-      auto issuer = [&](auto tile) {
-        constexpr int t = decltype(tile)::value;
-        const int ksteps = (p.dh + 15) / 16;
-        constexpr uint32_t idesc_qk = idesc_f16kind_f32(BM, BN, false, C::F16);
-        const uint32_t idesc_pv = idesc_f16kind_f32(BM, 16, true, C::F16) + (static_cast<uint32_t>((ksteps * 16 - 16) >> 3) << 17);
-        const uint32_t tS = tmem + t * C::TM_TILE, tP = tS + C::TM_P, tO = tS + C::TM_O;
-        // Descriptors count addresses in units of 16 bytes.
-        const uint64_t q_desc = smem_desc(sbase + t * C::Q_TILE, 16, 1024), k_desc = smem_desc(sbase + C::K_OFF, 16, 1024);
-        const uint64_t v_desc = smem_desc(sbase + C::V_OFF, BN * 128, 1024);
-        const Bounds mine = tb[t];
-        auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, p.err)) != 0; };
-        auto issue_qk = [&](int s) {
-          const uint64_t kd = k_desc + static_cast<uint32_t>(s * (C::KV_TILE / 16));
-          if (elect_one()) {
+      const int ksteps = (p.dh + 15) / 16;
+      constexpr uint32_t idesc_qk = idesc_f16kind_f32(BM, BN, false, C::F16);
+      const uint32_t idesc_pv = idesc_f16kind_f32(BM, 16, true, C::F16) + (static_cast<uint32_t>((ksteps * 16 - 16) >> 3) << 17);
+      const uint32_t tS = tmem, tP = tmem + C::TM_P, tO = tmem + C::TM_O;
+      // Descriptors count addresses in units of 16 bytes.
+      const uint64_t q_desc = smem_desc(sbase, 16, 1024), k_desc = smem_desc(sbase + C::K_OFF, 16, 1024);
+      const uint64_t v_desc = smem_desc(sbase + C::V_OFF, BN * 128, 1024);
+      auto wait = [&](uint32_t bar, int parity) { return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, p.err)) != 0; };
+      auto issue_qk = [&](int s) {
+        const uint64_t kd = k_desc + static_cast<uint32_t>(s * (C::KV_TILE / 16));
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < C::DHT / 16; ++ks)
-              if (ks < ksteps)
-                mma_ss(tS, q_desc + (ks >> 2) * (BM * 8) + (ks & 3) * 2, kd + (ks >> 2) * (BN * 8) + (ks & 3) * 2, idesc_qk,
-                       ks > 0 ? 1u : 0u);
-            mma_commit(bars.s_full(t));
-          }
-          __syncwarp();
-        };
-        auto issue_pv = [&](int s, bool first) {
-          const uint64_t vd = v_desc + static_cast<uint32_t>(s * (C::KV_TILE / 16));
-          if (elect_one()) {
-#pragma unroll
-            for (int ks = 0; ks < BN / 16; ++ks) mma_ts(tO, tP + ks * 8, vd + ks * 128, idesc_pv, (!first || ks > 0) ? 1u : 0u);
-            mma_commit(bars.o_done(t));
-            mma_commit(bars.kv_empty(s));
-          }
-          __syncwarp();
-        };
-        // S of the next tile is issued before P V of this one, as soon as S has been read; where P lies
-        // over S, once P V is complete. Key tiles that this query tile does not need are released as
-        // they arrive, after the P V that is still to come: its own stage must not wait for them.
-        bool ok = j1 <= j0 || wait(bars.q_full(), 0);
-        int n = 0, pending = -1, pending_parity = 0;  // S issued so far; stage of the tile whose P V is still to come
-        auto finish = [&] {
-          if (pending < 0) return true;
-          if (!wait(bars.p_full(t), (n - 1) & 1) || !wait(bars.v_ready(pending), pending_parity)) return false;
-          tc_fence_after();
-          issue_pv(pending, n == 1);
-          pending = -1;
-          return true;
-        };
-        int s = 0, parity = 0;  // ring position
-        for (int j = j0; ok && j < j1; ++j) {
-          const bool held = mine.template holds<BN>(j);
-          if ((!held || !C::P_SEP) && !(ok = finish())) break;
-          if (!(ok = wait(bars.k_full(s), parity))) break;
-          if (!held) {
-            if (lane == 0) mbar_arrive(bars.kv_empty(s));
-          } else {
-            if (n > 0 && !(ok = wait(C::P_SEP ? bars.s_free(t) : bars.o_done(t), (n - 1) & 1))) break;
-            tc_fence_after();
-            issue_qk(s);
-            if (C::P_SEP && !(ok = finish())) break;  // (its counts are those before this S)
-            ++n;
-            pending = s;
-            pending_parity = parity;
-          }
-          if (++s == STAGES) s = 0, parity ^= 1;
+          for (int ks = 0; ks < C::DHT / 16; ++ks)
+            if (ks < ksteps)
+              mma_ss(tS, q_desc + (ks >> 2) * (BM * 8) + (ks & 3) * 2, kd + (ks >> 2) * (BN * 8) + (ks & 3) * 2, idesc_qk,
+                     ks > 0 ? 1u : 0u);
+          mma_commit(bars.s_full());
+          mma_commit(bars.k_empty(s));
         }
-        if (ok) finish();
-        if (elect_one()) mma_commit(bars.fin(t));
-        wait_bar(bars.fin(t), 0, abort_flag, p.err, false);
+        __syncwarp();
       };
-      if (warp == 1) issuer(std::integral_constant<int, 0>());
-      else if constexpr (NQ == 2) issuer(std::integral_constant<int, 1>());
+      auto issue_pv = [&](int s, bool first) {
+        const uint64_t vd = v_desc + static_cast<uint32_t>(s * (C::KV_TILE / 16));
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < BN / 16; ++ks) mma_ts(tO, tP + ks * 8, vd + ks * 128, idesc_pv, (!first || ks > 0) ? 1u : 0u);
+          mma_commit(bars.o_done());
+          mma_commit(bars.v_empty(s));
+        }
+        __syncwarp();
+      };
+      // S of the next tile is issued before P V of this one, as soon as S has been read; where P lies
+      // over S, once P V is complete.
+      bool ok = j1 <= j0 || wait(bars.q_full(), 0);
+      Ring<KS> rk;
+      Ring<VS> rv;
+      auto finish = [&](int n) {  // P V of the n-th tile
+        if (!wait(bars.p_full(), n & 1) || !wait(bars.v_ready(rv.s), rv.parity)) return false;
+        issue_pv(rv.s, n == 0);
+        rv.next();
+        return true;
+      };
+      int n = 0;
+      for (int j = j0; ok && j < j1; ++j, ++n) {
+        if (!C::P_SEP && n > 0 && !(ok = finish(n - 1))) break;
+        if (!(ok = wait(bars.k_full(rk.s), rk.parity))) break;
+        if (n > 0 && !(ok = wait(C::P_SEP ? bars.s_free() : bars.o_done(), (n - 1) & 1))) break;
+        issue_qk(rk.s);
+        rk.next();
+        if (C::P_SEP && n > 0 && !(ok = finish(n - 1))) break;
+      }
+      if (ok && n > 0) finish(n - 1);
+      if (elect_one()) mma_commit(bars.fin());
+      wait_bar(bars.fin(), 0, abort_flag, p.err, false);
       __syncwarp();
-    } else if (warp == 3) {
+    } else if (warp == 2) {
       // ---------------------------------------------------------------- guard
-      int g = 0;
-      for (int j = j0; j < j1; ++j, ++g) {
-        const int s = g % STAGES;
+      Ring<VS> rv;
+      for (int j = j0; j < j1; ++j) {
+        const int s = rv.s;
         if constexpr (C::BIAS) {
-          if (g >= STAGES && !__all_sync(0xffffffffu, wait_bar(bars.kv_empty(s), (g / STAGES - 1) & 1, abort_flag, p.err))) break;
+          if (j - j0 >= VS && !__all_sync(0xffffffffu, wait_bar(bars.v_empty(s), rv.parity ^ 1, abort_flag, p.err))) break;
           // Window value e belongs to the distance d0 + e.
-          const long long d0 = static_cast<long long>(j) * BN - (row0 / p.pack + NQ * BM - 1) + shift0;
+          const long long d0 = static_cast<long long>(j) * BN - (row0 / p.pack + BM - 1) + shift0;
           const float* table = p.bias + static_cast<long long>(h0) * (2LL * p.radius + 1) + p.radius;
           float* w = reinterpret_cast<float*>(smem + C::BIAS_OFF) + s * C::WINDOW;
 #pragma unroll
-          for (int i = 0; i < C::WINDOW / 32; ++i) {
-            const float x = __ldg(table + clampll(d0 + i * 32 + lane, -p.radius, p.radius));
-            const float y = x * 1.4426950408889634f;
-            // the lowest finite value stays finite in units of log2
-            w[i * 32 + lane] = isinf(y) && !isinf(x) ? copysignf(3.402823466e38f, x) : y;
-          }
+          for (int i = 0; i < C::WINDOW / 32; ++i)
+            w[i * 32 + lane] = bias_log2(__ldg(table + clampll(d0 + i * 32 + lane, -p.radius, p.radius)));
           __syncwarp();
           if (lane == 0) mbar_arrive(bars.bias_full(s));
         }
-        if (!__all_sync(0xffffffffu, wait_bar(bars.v_full(s), (g / STAGES) & 1, abort_flag, p.err))) break;
-        bool masks = false;
-#pragma unroll
-        for (int t = 0; t < NQ; ++t) masks |= tb[t].template holds<BN>(j) && !tb[t].template whole<BN>(j);
-        if (masks) {
+        if (!__all_sync(0xffffffffu, wait_bar(bars.v_full(s), rv.parity, abort_flag, p.err))) break;
+        if (j < whole0 || j >= whole1) {
           uint4* tile = reinterpret_cast<uint4*>(smem + C::V_OFF + s * C::KV_TILE);
-          const int n = chunks * BN * 8;
-          constexpr uint32_t kExp = C::F16 ? 0x7c00u : 0x7f80u;  // all exponent bits set: infinity or NaN
-          bool found = false;
-          for (int i = lane; i < n; i += 32) {
-            uint4 x = tile[i];
-            uint32_t* w = reinterpret_cast<uint32_t*>(&x);
-            bool bad = false;
+          if (__any_sync(0xffffffffu, !all_finite<C::F16>(tile, chunks * BN * 8, lane))) {
+            for (int i = lane; i < chunks * BN * 8; i += 32) {
+              uint4 x = tile[i];
+              uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+              constexpr uint32_t kExp = C::F16 ? 0x7c00u : 0x7f80u;  // all exponent bits set: infinity or NaN
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if ((w[k] & kExp) == kExp) w[k] &= 0xffff0000u, bad = true;
-              if ((w[k] >> 16 & kExp) == kExp) w[k] &= 0xffffu, bad = true;
+              for (int k = 0; k < 4; ++k) {
+                if ((w[k] & kExp) == kExp) w[k] &= 0xffff0000u;
+                if ((w[k] >> 16 & kExp) == kExp) w[k] &= 0xffffu;
+              }
+              tile[i] = x;
             }
-            if (bad) tile[i] = x, found = true;
-          }
-          if (__any_sync(0xffffffffu, found)) {
             if (lane == 0) *cleaned = 1;
             fence_proxy_async_smem();
             __syncwarp();
           }
         }
         if (lane == 0) mbar_arrive(bars.v_ready(s));
+        rv.next();
       }
     }
   } else {
-    // ================================================================== softmax warpgroups
-    if constexpr (NQ == 2) regs_inc<C::REG_SOFT>();
-    const int t = NQ == 1 ? 0 : warp >> 3, quarter = warp & 3;
-    const uint32_t tbase = tmem + t * C::TM_TILE + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t tS = tbase, tP = tbase + C::TM_P, tO = tbase + C::TM_O;
-    const Bounds mine = NQ == 2 && t == 1 ? tb[NQ - 1] : tb[0];
+    // ================================================================== softmax warps
+    if constexpr (C::CTAS == 2) regs_inc<C::REG_SOFT>();
+    constexpr int HC = C::HC;
+    const int quarter = warp & 3;
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t tS = tbase + half * HC, tP = tbase + C::TM_P + half * (HC / 2), tO = tbase + C::TM_O;
     const bool live = row0 + (r_in & ~31) < rows;  // a warp behind the last row only keeps the barriers going
     const bool is_mixed = C::BIAS && *mixed;
     const int ochunks = (p.dh + 15) / 16;
-    // This tile's key tiles, [jf, jl) of the CTA's; element masks outside [wf, wl).
-    const int jf = max(j0, mine.template first<BN>()), jl = mine.empty() ? jf : min(j1, mine.template last<BN>());
-    const int wf = (mine.lo_last + BN - 1) / BN, wl = mine.hi_first / BN;
-    // Turns: where both query tiles need a key tile, their warps on one SM sub-partition take its
-    // special-function unit one after the other (tile 0 first), so that one tile's exp2 phase overlaps
-    // the other's maxima, loads, stores and MMAs. Tile t waits for turn(t), and passes the turn on.
-    int both0 = 0, both1 = 0;
-    if (NQ == 2 && !tb[0].empty() && !tb[NQ - 1].empty()) {
-      both0 = max(tb[0].template first<BN>(), tb[NQ - 1].template first<BN>());
-      both1 = min(tb[0].template last<BN>(), tb[NQ - 1].template last<BN>());
-    }
-    auto take_turn = [&](int j) {
-      if (t == 0 && j == both0) return true;
-      return __all_sync(0xffffffffu, wait_bar(bars.turn(t, quarter), (t == 0 ? j - both0 - 1 : j - both0) & 1, abort_flag, p.err)) != 0;
-    };
-    auto pass_turn = [&] {
+    // Exchange with the thread of the row's other half, one phase of the two warps' barrier each time. The
+    // two buffers alternate: a value is overwritten two phases on, after the other warp has read it.
+    volatile float* xch = reinterpret_cast<volatile float*>(smem + C::XCH_OFF) + r_in;
+    auto other_half = [&](float v, int phase, float& theirs) {
+      xch[((phase & 1) * 2 + half) * BM] = v;
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars.turn(1 - t, quarter));
+      if (lane == 0) mbar_arrive(bars.halves(quarter));
+      const bool met = __all_sync(0xffffffffu, wait_bar(bars.halves(quarter), phase & 1, abort_flag, p.err));
+      theirs = xch[((phase & 1) * 2 + (half ^ 1)) * BM];
+      return met;
     };
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     if (!live) {
-      for (int j = jf; ok && j < jl; ++j) {
-        const int par = (j - jf) & 1;
-        ok = __all_sync(0xffffffffu, wait_bar(bars.s_full(t), par, abort_flag, p.err));
-        if (ok && C::P_SEP) mbar_arrive(bars.s_free(t));
+      for (int j = j0; ok && j < j1; ++j) {
+        const int par = (j - j0) & 1;
+        ok = __all_sync(0xffffffffu, wait_bar(bars.s_full(), par, abort_flag, p.err));
+        if (ok && C::P_SEP) mbar_arrive(bars.s_free());
         // as the other warps: no arrival for this P before every warp's for the one before it
-        if (ok && j > jf) ok = __all_sync(0xffffffffu, wait_bar(bars.o_done(t), par ^ 1, abort_flag, p.err));
-        if (ok) mbar_arrive(bars.p_full(t));
-        if (NQ == 2 && ok && j >= both0 && j < both1) {
-          ok = take_turn(j);
-          if (ok) pass_turn();
-        }
+        if (ok && j > j0) ok = __all_sync(0xffffffffu, wait_bar(bars.o_done(), par ^ 1, abort_flag, p.err));
+        if (ok) mbar_arrive(bars.p_full());
       }
     }
-    for (int j = jf; live && j < jl; ++j) {
-      if (!__all_sync(0xffffffffu, wait_bar(bars.s_full(t), (j - jf) & 1, abort_flag, p.err))) {
+    for (int j = j0; live && j < j1; ++j) {
+      // warp-uniform: the tcgen05 copies below are .sync.aligned
+      if (!__all_sync(0xffffffffu, wait_bar(bars.s_full(), (j - j0) & 1, abort_flag, p.err))) {
         ok = false;
         break;
       }
-      if (C::BIAS && !__all_sync(0xffffffffu, wait_bar(bars.bias_full((j - j0) % STAGES), ((j - j0) / STAGES) & 1, abort_flag, p.err))) {
+      if (C::BIAS && !__all_sync(0xffffffffu, wait_bar(bars.bias_full((j - j0) % VS), ((j - j0) / VS) & 1, abort_flag, p.err))) {
         ok = false;
         break;
       }
       tc_fence_after();
-      float sv[BN];
+      float sv[HC];
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) {
+      for (int c = 0; c < HC / 32; ++c) {
         uint32_t r[32];
         tmem_ld32(tS + c * 32, r);
 #pragma unroll
@@ -547,47 +556,59 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       tmem_wait_ld();
       if constexpr (C::P_SEP) {
         tc_fence_before();
-        mbar_arrive(bars.s_free(t));
+        mbar_arrive(bars.s_free());
       }
       if constexpr (C::CAP) {
         // cap log2(e) tanh(x / cap) = cap log2(e) (1 - 2 / (1 + exp(2 x / cap)))
 #pragma unroll
-        for (int i = 0; i < BN; ++i)
+        for (int i = 0; i < HC; ++i)
           sv[i] = fmaf(-2.f * p.cap_out, rcp_approx(1.f + ex2_approx(sv[i] * p.cap_in)), p.cap_out);
       }
       if constexpr (C::BIAS) {
         if (!is_mixed) {
-          const float* w = reinterpret_cast<const float*>(smem + C::BIAS_OFF) + ((j - j0) % STAGES) * C::WINDOW + (NQ * BM - 1 - r_in);
+          const float* w = reinterpret_cast<const float*>(smem + C::BIAS_OFF) + ((j - j0) % VS) * C::WINDOW + (BM - 1 - r_in) + half * HC;
 #pragma unroll
-          for (int i = 0; i < BN; ++i) sv[i] = C::CAP ? sv[i] + w[i] : fmaf(sv[i], p.scale_log2, w[i]);
+          for (int i = 0; i < HC; ++i) sv[i] = C::CAP ? sv[i] + w[i] : fmaf(sv[i], p.scale_log2, w[i]);
         } else {  // a tile over documents with different shifts: each row its own distances
           const float* table = p.bias + static_cast<long long>(h0) * (2LL * p.radius + 1) + p.radius;
-          const long long d0 = static_cast<long long>(j) * BN - (row0 + r_in) / p.pack + me.shift;
+          const long long d0 = static_cast<long long>(j) * BN + half * HC - (row0 + r_in) / p.pack + me.shift;
 #pragma unroll
-          for (int i = 0; i < BN; ++i) {
-            const float x = __ldg(table + clampll(d0 + i, -p.radius, p.radius));
-            float y = x * 1.4426950408889634f;
-            if (isinf(y) && !isinf(x)) y = copysignf(3.402823466e38f, x);
+          for (int i = 0; i < HC; ++i) {
+            const float y = bias_log2(__ldg(table + clampll(d0 + i, -p.radius, p.radius)));
             sv[i] = C::CAP ? sv[i] + y : fmaf(sv[i], p.scale_log2, y);
           }
         }
       }
-      if (__builtin_expect(j < wf || j >= wl, 0)) {
-        const int lo = me.lo - j * BN, hi = me.hi - j * BN;
+      if (j < whole0 || j >= whole1) {
+        // Element masks, 32 columns at a time: a warp's rows mostly see all or nothing of them.
+        const int lo = me.lo - j * BN - half * HC, hi = me.hi - j * BN - half * HC;
 #pragma unroll
-        for (int i = 0; i < BN; ++i)
-          if (i < lo || i >= hi) sv[i] = -INFINITY;
+        for (int w = 0; w < HC / 32; ++w) {
+          const int l = min(max(lo - 32 * w, 0), 32), h = min(max(hi - 32 * w, 0), 32);
+          const uint32_t seen = static_cast<uint32_t>(((1ull << h) - 1) & ~((1ull << l) - 1));
+          if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sv[32 * w + i] = seen >> i & 1 ? sv[32 * w + i] : -INFINITY;
+          }
+        }
       }
       float pm[8];
 #pragma unroll
       for (int k = 0; k < 8; ++k) pm[k] = sv[k];
 #pragma unroll
-      for (int i = 8; i + 16 <= BN; i += 16)
+      for (int i = 8; i + 16 <= HC; i += 16)
 #pragma unroll
         for (int k = 0; k < 8; ++k) pm[k] = max3f(pm[k], sv[i + k], sv[i + 8 + k]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], sv[BN - 8 + k]);
-      const float mx = max3f(max3f(pm[0], pm[1], pm[2]), max3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+      for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], sv[HC - 8 + k]);
+      float mx = max3f(max3f(pm[0], pm[1], pm[2]), max3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])), theirs;
+      if constexpr (HALVES == 2) {
+        if (!other_half(mx, j - j0, theirs)) {
+          ok = false;
+          break;
+        }
+        mx = fmaxf(mx, theirs);
+      }
       constexpr bool kLog2 = C::CAP || C::BIAS;  // sv is in units of log2 already
       const float m_new = fmaxf(m_run, kLog2 ? mx : mx * p.scale_log2);
       // Row by row: no row's bits depend on its neighbours' scores.
@@ -595,16 +616,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       const float alpha = !raise ? 1.0f : m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
       if (raise) m_run = m_new;
       const float neg_m = m_run == -INFINITY ? 0.f : -m_run;  // a row that has seen nothing: all its exp2 are 0
-      const bool turns = NQ == 2 && j >= both0 && j < both1;
-      if (turns && !take_turn(j)) {
-        ok = false;
-        break;
-      }
-      uint32_t pk[BN / 2];
+      uint32_t pk[HC / 2];
       float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
 #pragma unroll
-      for (int i = 0; i < BN / 2; ++i) {
-        if (i == C::PASS && turns) pass_turn();
+      for (int i = 0; i < HC / 2; ++i) {
         float x0, x1;
         if constexpr (kLog2) add2(x0, x1, sv[2 * i], sv[2 * i + 1], neg_m, neg_m);
         else fma2(x0, x1, sv[2 * i], sv[2 * i + 1], p.scale_log2, p.scale_log2, neg_m, neg_m);
@@ -619,14 +634,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         pk[i] = C::F16 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
       }
       l_run = fmaf(l_run, alpha, (ls0 + ls1) + (ls2 + ls3));
-      if (j > jf) {
-        if (!__all_sync(0xffffffffu, wait_bar(bars.o_done(t), (j - jf - 1) & 1, abort_flag, p.err))) {
+      if (j > j0) {
+        if (!__all_sync(0xffffffffu, wait_bar(bars.o_done(), (j - j0 - 1) & 1, abort_flag, p.err))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (rescale) {
-          for (int c = 0; c < ochunks; ++c) {
+        if (rescale) {  // the two halves take every other 16 columns of O
+          for (int c = half; c < ochunks; c += HALVES) {
             uint32_t r[16];
             tmem_ld16(tO + c * 16, r);
             tmem_wait_ld();
@@ -637,7 +652,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
 #pragma unroll
-      for (int c = 0; c < BN / 32; ++c) {
+      for (int c = 0; c < HC / 32; ++c) {
         uint32_t r[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) r[i] = pk[c * 16 + i];
@@ -645,21 +660,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(bars.p_full(t));
+      mbar_arrive(bars.p_full());
     }
-    if (ok && jl > jf) ok = __all_sync(0xffffffffu, wait_bar(bars.o_done(t), (jl - jf - 1) & 1, abort_flag, p.err));
+    if (ok && j1 > j0) ok = __all_sync(0xffffffffu, wait_bar(bars.o_done(), (j1 - j0 - 1) & 1, abort_flag, p.err));
     tc_fence_after();
-    // ------------------------------------------------------------------ epilogue, one row a thread
+    if (HALVES == 2 && live && ok && j1 > j0) {
+      float theirs;
+      ok = other_half(l_run, j1 - j0, theirs);
+      l_run = half ? theirs + l_run : l_run + theirs;
+    }
+    // ------------------------------------------------------------------ epilogue: every other 16 columns of a row
     const long long row = row0 + r_in;
     const int i_q = static_cast<int>(row / p.pack), h = h0 + static_cast<int>(row % p.pack);
     // Values that the guard set to zero, for rows that see them: 16 columns from c16 of the masked tiles.
     auto add_cleaned = [&](int c16, float (&o)[16]) {
       const uint16_t* v = p.v + b * p.v_batch + kvh * p.v_head + c16;
       for (int j = j0; j < j1; ++j) {
-        bool masks = false;
-#pragma unroll
-        for (int u = 0; u < NQ; ++u) masks |= tb[u].template holds<BN>(j) && !tb[u].template whole<BN>(j);
-        if (!masks) continue;
+        if (j >= whole0 && j < whole1) continue;
         for (int key = max(me.lo, j * BN); key < min(me.hi, (j + 1) * BN); ++key) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -673,15 +690,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
       }
     };
-    const bool has_o = jl > jf && ok, fix = has_o && *cleaned;  // the same for the warp
-    const bool join = NQ == 1 && splits > 1;
+    const bool has_o = j1 > j0 && ok, fix = has_o && *cleaned;  // the same for the warp
+    const bool join = splits > 1;
     const bool store = row < rows && (join || (me.exists && ok));
-    // A part of a cluster's join goes over the ring: its copies and MMAs are done with the last P V.
-    float* part = reinterpret_cast<float*>(smem + C::K_OFF) + (NQ == 1 ? r_in : 0) * C::JOIN_ROW;
+    // A part of a cluster's join goes over Q and the ring: their copies and MMAs are done with the last P V.
+    float* part = reinterpret_cast<float*>(smem) + r_in * C::JOIN_ROW;
     uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.o_batch + i_q * p.o_token + h * p.o_head;
     const float inv = join ? 1.f : l_run == 0.f ? 0.f : 1.0f / l_run;
     if (live) {
-      for (int c = 0; c < ochunks; ++c) {
+      for (int c = half; c < ochunks; c += HALVES) {
         float o[16];
         if (has_o) {  // warp-wide: every lane takes part
           uint32_t r[16];
@@ -709,7 +726,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
           if (c * 16 + 8 < p.dh) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
       }
-      if (join && store) {
+      if (join && store && half == 0) {
         part[C::DHT] = m_run;
         part[C::DHT + 1] = l_run;
       }
@@ -721,42 +738,38 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::TM_COLS);
   }
-  if constexpr (NQ == 1) {
-    if (splits > 1) {
-      // Join: the rows are dealt to the CTAs; each output value is summed over the parts in rank order.
-      cluster_sync();
-      const int live_rows = static_cast<int>(min(rows - row0, static_cast<long long>(BM)));
-      const int groups = p.dh / 8;  // 8 columns a thread
-      const uint32_t base = sbase + C::K_OFF;
-      if (!*abort_flag)
-        for (int w = rank * C::THREADS + static_cast<int>(threadIdx.x); w < live_rows * groups; w += splits * C::THREADS) {
-          const int r = w / groups, c = w % groups * 8;
-          const Row info = row_of(p, b, static_cast<int>((row0 + r) / p.pack));
-          float m = -INFINITY;
-          for (int k = 0; k < splits; ++k) m = fmaxf(m, peer_load4(base + (r * C::JOIN_ROW + C::DHT) * 4, k).x);
-          float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          for (int k = 0; k < splits; ++k) {
-            const float4 ml = peer_load4(base + (r * C::JOIN_ROW + C::DHT) * 4, k);
-            if (ml.y == 0.f) continue;  // this part has no key that the row sees
-            const float a = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
-            const float4 x = peer_load4(base + (r * C::JOIN_ROW + c) * 4, k);
-            const float4 y = peer_load4(base + (r * C::JOIN_ROW + c + 4) * 4, k);
-            l = fmaf(ml.y, a, l);
-            o[0] = fmaf(x.x, a, o[0]), o[1] = fmaf(x.y, a, o[1]), o[2] = fmaf(x.z, a, o[2]), o[3] = fmaf(x.w, a, o[3]);
-            o[4] = fmaf(y.x, a, o[4]), o[5] = fmaf(y.y, a, o[5]), o[6] = fmaf(y.z, a, o[6]), o[7] = fmaf(y.w, a, o[7]);
-          }
-          if (!info.exists) continue;
-          const float inv = l == 0.f ? 0.f : 1.0f / l;
-          uint32_t q[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            q[i] = C::F16 ? pack_f16x2(o[2 * i] * inv, o[2 * i + 1] * inv) : pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
-          const long long at = row0 + r;
-          uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.o_batch + (at / p.pack) * p.o_token + (h0 + at % p.pack) * p.o_head;
-          *reinterpret_cast<uint4*>(out + c) = make_uint4(q[0], q[1], q[2], q[3]);
+  if (splits > 1) {
+    // Join: the rows are dealt to the CTAs; each output value is summed over the parts in rank order.
+    cluster_sync();
+    const int live_rows = static_cast<int>(min(rows - row0, static_cast<long long>(BM)));
+    const int groups = p.dh / 8;  // 8 columns a thread
+    if (!*abort_flag)
+      for (int w = rank * C::THREADS + static_cast<int>(threadIdx.x); w < live_rows * groups; w += splits * C::THREADS) {
+        const int r = w / groups, c = w % groups * 8;
+        const long long at = row0 + r;
+        if (!row_of(p, b, static_cast<int>(at / p.pack)).exists) continue;
+        float m = -INFINITY;
+        for (int k = 0; k < splits; ++k) m = fmaxf(m, peer_load4(sbase + (r * C::JOIN_ROW + C::DHT) * 4, k).x);
+        float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < splits; ++k) {
+          const float4 ml = peer_load4(sbase + (r * C::JOIN_ROW + C::DHT) * 4, k);
+          if (ml.y == 0.f) continue;  // this part has no key that the row sees
+          const float a = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
+          const float4 x = peer_load4(sbase + (r * C::JOIN_ROW + c) * 4, k);
+          const float4 y = peer_load4(sbase + (r * C::JOIN_ROW + c + 4) * 4, k);
+          l = fmaf(ml.y, a, l);
+          o[0] = fmaf(x.x, a, o[0]), o[1] = fmaf(x.y, a, o[1]), o[2] = fmaf(x.z, a, o[2]), o[3] = fmaf(x.w, a, o[3]);
+          o[4] = fmaf(y.x, a, o[4]), o[5] = fmaf(y.y, a, o[5]), o[6] = fmaf(y.z, a, o[6]), o[7] = fmaf(y.w, a, o[7]);
         }
-      cluster_sync();  // no CTA leaves while a peer reads its part
-    }
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        uint32_t q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          q[i] = C::F16 ? pack_f16x2(o[2 * i] * inv, o[2 * i + 1] * inv) : pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
+        uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.o_batch + (at / p.pack) * p.o_token + (h0 + at % p.pack) * p.o_head;
+        *reinterpret_cast<uint4*>(out + c) = make_uint4(q[0], q[1], q[2], q[3]);
+      }
+    cluster_sync();  // no CTA leaves while a peer reads its part
   }
 }
 

@@ -1,7 +1,10 @@
-// sd_attention_masked for heads of up to 64 columns: S, P and O of two query tiles side by side fill
-// tensor memory; four stages of 16 KB key and value tiles.
+// sd_attention_masked for heads of up to 64 columns.
 #include "attention_masked_launch.cuh"
 
+#ifndef V
+#define V 2, 2, 2
+#define VSEP true
+#endif
 sd_status sd::masked::launch_dh64(const Launch& l) {
-  return l.args->dtype ? by_score<64, 128, 2, 4, 6, true, true, true>(l) : by_score<64, 128, 2, 4, 6, true, true, false>(l);
+  return l.args->dtype ? by_score<64, 128, V, VSEP, true>(l) : by_score<64, 128, V, VSEP, false>(l);
 }

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <algorithm>
+#include <cstdlib>
 #include <atomic>
 
 #include "attention_masked.cuh"
@@ -34,6 +35,12 @@ sd_status launch(const Launch& l, int pack, int64_t tiles, int splits) {
   p.docs = a.q_offsets ? static_cast<int>(a.docs) : 0;
   p.radius = static_cast<int>(a.bias_radius), p.causal = a.causal;
   p.tiles = static_cast<int>(tiles);
+  p.planes = static_cast<int>(a.B * (a.heads / pack));
+  // Where items differ in length, as many planes are mixed as have 48 MB of keys and values (half of L2).
+  const int64_t plane_bytes = std::max<int64_t>(a.Lk * a.dh * 4 * pack / l.group, 1);
+  p.plane_group = a.causal || a.q_offsets || a.kv_lens
+                      ? static_cast<int>(std::min<int64_t>(std::max<int64_t>((int64_t(48) << 20) / plane_bytes, 1), p.planes))
+                      : 1;
   constexpr float kLog2e = 1.4426950408889634f;
   p.scale_log2 = std::max(a.scale * kLog2e, 1.17549435e-38f);  // scale 0: a masked score must not become 0 * -infinity
   p.cap_in = C::CAP ? 2.f * kLog2e * (a.scale / a.cap) : 0.f;
@@ -72,37 +79,29 @@ sd_status launch(const Launch& l, int pack, int64_t tiles, int splits) {
   return sd::cuda_check(cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, p), "sd_attention_masked launch");
 }
 
-// Two = the configuration of two query tiles a CTA (one where tensor memory holds no more), One = of one.
-template <class Two, class One>
+template <class C>
 sd_status choose(const Launch& l) {
   const sd_attention_masked_args& a = *l.args;
   // Heads that share a key head become rows of one tile while that fills tiles better: few queries.
   // (The bias of a row's head would differ within a tile.)
   int pack = 1;
-  if (!One::BIAS && a.Lq <= BM / 2 && l.group > 1 && BM % l.group == 0) pack = static_cast<int>(l.group);
-  const int64_t planes = a.B * (a.heads / pack), rows = a.Lq * pack;
-  const int64_t one = (rows + BM - 1) / BM, two = (rows + 2 * BM - 1) / (2 * BM);
-  // One tile a CTA while each can have an SM of its own.
-  if (Two::NQ == 1 || planes * one <= sd::sm_count()) {
-    // Idle SMs: split the keys over a cluster, two key tiles a CTA at least.
-    int splits = 1;
-    const int64_t key_tiles = (a.Lk + One::BN - 1) / One::BN;
-    while (2 * splits <= kMaxSplits && planes * one * 2 * splits <= sd::sm_count() && key_tiles >= 4 * splits) splits *= 2;
-    return launch<One>(l, pack, one, splits);
-  }
-  return launch<Two>(l, pack, two, 1);
+  if (!C::BIAS && a.Lq <= BM / 2 && l.group > 1 && BM % l.group == 0) pack = static_cast<int>(l.group);
+  const int64_t planes = a.B * (a.heads / pack), tiles = (a.Lq * pack + BM - 1) / BM;
+  // Idle SMs: split the keys over a cluster, two key tiles a CTA at least.
+  int splits = 1;
+  const int64_t key_tiles = (a.Lk + C::BN - 1) / C::BN;
+  while (2 * splits <= kMaxSplits && planes * tiles * 2 * splits <= C::CTAS * sd::sm_count() && key_tiles >= 4 * splits) splits *= 2;
+  if (const char* e = getenv("SPLITS")) splits = atoi(e);
+  return launch<C>(l, pack, tiles, splits);
 }
 
-template <int DHT, int BN, int NQ2, int STAGES2, int STAGES1, bool P_SEP2, bool P_SEP1, bool F16>
+template <int DHT, int BN, int KS, int VS, int CTAS, bool P_SEP, bool F16>
 sd_status by_score(const Launch& l) {
   const bool cap = l.args->cap != 0.f, bias = l.args->bias != nullptr;
-  if (cap && bias)
-    return choose<Cfg<DHT, BN, NQ2, STAGES2, P_SEP2, F16, true, true>, Cfg<DHT, BN, 1, STAGES1, P_SEP1, F16, true, true>>(l);
-  if (cap)
-    return choose<Cfg<DHT, BN, NQ2, STAGES2, P_SEP2, F16, true, false>, Cfg<DHT, BN, 1, STAGES1, P_SEP1, F16, true, false>>(l);
-  if (bias)
-    return choose<Cfg<DHT, BN, NQ2, STAGES2, P_SEP2, F16, false, true>, Cfg<DHT, BN, 1, STAGES1, P_SEP1, F16, false, true>>(l);
-  return choose<Cfg<DHT, BN, NQ2, STAGES2, P_SEP2, F16, false, false>, Cfg<DHT, BN, 1, STAGES1, P_SEP1, F16, false, false>>(l);
+  if (cap && bias) return choose<Cfg<DHT, BN, KS, VS, CTAS, P_SEP, F16, true, true>>(l);
+  if (cap) return choose<Cfg<DHT, BN, KS, VS, CTAS, P_SEP, F16, true, false>>(l);
+  if (bias) return choose<Cfg<DHT, BN, KS, VS, CTAS, P_SEP, F16, false, true>>(l);
+  return choose<Cfg<DHT, BN, KS, VS, CTAS, P_SEP, F16, false, false>>(l);
 }
 
 }  // namespace masked
