@@ -59,7 +59,7 @@ struct Params {
   int tiles;             // query tiles of a plane (one batch's packed head)
   int planes, plane_group;  // planes; planes whose items are mixed
   float scale_log2;      // scale * log2(e)
-  float cap_in, cap_out; // 2 log2(e) scale / cap, cap log2(e)
+  float cap_in, cap_out; // scale / cap, cap log2(e)
   unsigned int* err;
 };
 
@@ -120,41 +120,30 @@ template <int DHT_, int BN_, int KS_, int VS_, int CTAS_, bool P_SEP_, bool F16_
 struct Cfg {
   static constexpr int DHT = DHT_, BN = BN_, KS = KS_, VS = VS_, CTAS = CTAS_;
   static constexpr bool P_SEP = P_SEP_, F16 = F16_, CAP = CAP_, BIAS = BIAS_;
-#ifndef HV
-#define HV 1
-#endif
-  static constexpr int HALVES = HV;        // threads that share a row
-  static constexpr int HC = BN / HALVES;   // columns of a softmax thread
   static constexpr int NCH = (DHT + 63) / 64;
   static constexpr int Q_TILE = NCH * BM * 128, KV_TILE = NCH * BN * 128;
   static constexpr int K_OFF = Q_TILE, V_OFF = K_OFF + KS * KV_TILE;
   static constexpr int BIAS_OFF = V_OFF + VS * KV_TILE;
-  static constexpr int WINDOW = BM + BN;  // values of one bias window (one unused); one for each stage of V
-  // The two halves of a row exchange their maxima (two buffers) and, at the end, their sums.
-  static constexpr int XCH_OFF = BIAS_OFF + (BIAS ? VS * WINDOW * 4 : 0);
-  static constexpr int BAR_OFF = XCH_OFF + (HALVES == 2 ? 2 * 2 * BM * 4 : 0);
-  // q_full, s_full, s_free, p_full, o_done, fin, halves[4], k_full[KS], k_empty[KS], v_full[VS], v_ready[VS],
-  // v_empty[VS], bias_full[VS]
-  static constexpr int NBARS = 10 + 2 * KS + 4 * VS;
+  // Windows of a bias, one for each stage of V: the BM + BN - 1 values of a tile's distances, in four
+  // copies shifted by 1 to 4 values, so that every row reads its own 16 bytes at a time; eight
+  // neighbouring rows meet all banks once (WINDOW is 8 modulo 32).
+  static constexpr int WINDOW = BM + BN + 8;
+  static constexpr int BAR_OFF = BIAS_OFF + (BIAS ? VS * 4 * WINDOW * 4 : 0);
+  // q_full, s_full, s_free, p_full, o_done, fin, k_full[KS], k_empty[KS], v_full[VS], v_ready[VS], v_empty[VS],
+  // bias_full[VS]
+  static constexpr int NBARS = 6 + 2 * KS + 4 * VS;
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // TMEM address, abort flag, cleaned flag, mixed flag
   static constexpr int BOUNDS_OFF = MISC_OFF + 16;      // lo of the first and last row, hi of both
   static constexpr int SMEM = BOUNDS_OFF + 16;
   static constexpr int TM_P = P_SEP ? BN : 0, TM_O = P_SEP ? BN + BN / 2 : BN;
-  static constexpr int TM_COLS = TM_O + DHT <= 256 ? 256 : 512;
-  static constexpr int THREADS = 128 + 128 * HALVES;
-#ifndef RH
-#define RH 64
-#define RS 192
-#endif
-  static constexpr int REG_HELPER = RH, REG_SOFT = RS;  // two CTAs an SM: registers move to the softmax warps
-  // Of every 8 column pairs this many take exp2 on the FMA pipe; with a cap or bias that pipe has other work.
-#ifndef NPOLY
-#define NPOLY 2
-#endif
-  static constexpr int POLY = CAP || BIAS ? 0 : NPOLY;
+  static constexpr int TM_COLS = TM_O + DHT <= 128 ? 128 : TM_O + DHT <= 256 ? 256 : 512;
+  static constexpr int THREADS = 256;
+  static constexpr int REG_HELPER = 64, REG_SOFT = 192;  // two CTAs an SM: registers move to the softmax warps
   // Join of a cluster's parts: rows of DHT fp32 and (m, l), over Q and the rings.
   static constexpr int JOIN_ROW = DHT + 4;  // floats a row (+4: rows start in different banks)
   static_assert(CTAS * TM_COLS <= 512 && CTAS * (SMEM + 1024) <= 228 * 1024, "on-chip memory");
+  static_assert(CTAS == 1 || (CTAS == 2 && 128 * (REG_HELPER + REG_SOFT) <= 65536 / 2), "register split");
+  static_assert(!BIAS || WINDOW % 32 == 8, "copies of a window in different banks");
   static_assert(BM * JOIN_ROW * 4 <= Q_TILE + (KS + VS) * KV_TILE, "the join fits Q and the rings");
 };
 
@@ -167,13 +156,12 @@ struct Bars {
   __device__ uint32_t p_full() const { return base + 24; }
   __device__ uint32_t o_done() const { return base + 32; }
   __device__ uint32_t fin() const { return base + 40; }
-  __device__ uint32_t halves(int quarter) const { return base + 48 + 8 * quarter; }
-  __device__ uint32_t k_full(int s) const { return base + 8 * (10 + s); }
-  __device__ uint32_t k_empty(int s) const { return base + 8 * (10 + KS + s); }
-  __device__ uint32_t v_full(int s) const { return base + 8 * (10 + 2 * KS + s); }
-  __device__ uint32_t v_ready(int s) const { return base + 8 * (10 + 2 * KS + VS + s); }
-  __device__ uint32_t v_empty(int s) const { return base + 8 * (10 + 2 * KS + 2 * VS + s); }
-  __device__ uint32_t bias_full(int s) const { return base + 8 * (10 + 2 * KS + 3 * VS + s); }
+  __device__ uint32_t k_full(int s) const { return base + 8 * (6 + s); }
+  __device__ uint32_t k_empty(int s) const { return base + 8 * (6 + KS + s); }
+  __device__ uint32_t v_full(int s) const { return base + 8 * (6 + 2 * KS + s); }
+  __device__ uint32_t v_ready(int s) const { return base + 8 * (6 + 2 * KS + VS + s); }
+  __device__ uint32_t v_empty(int s) const { return base + 8 * (6 + 2 * KS + 2 * VS + s); }
+  __device__ uint32_t bias_full(int s) const { return base + 8 * (6 + 2 * KS + 3 * VS + s); }
 };
 
 // A position in a ring of N stages, and the parity of its phase.
@@ -189,6 +177,9 @@ struct Ring {
 struct Bounds {
   int lo_first, lo_last, hi_first, hi_last;
 };
+
+// Whether the distances d0 .. d0 + n - 1 all lie beyond the table's ends: one bias for all of them.
+__device__ __forceinline__ bool is_far(long long d0, int n, int radius) { return d0 >= radius || d0 + n - 1 <= -radius; }
 
 // Whether a lane's share of n packs of 16-bit values holds no infinity and no NaN: each value times
 // zero is zero, or NaN. Eight packs are in flight at a time (n is a multiple of 256).
@@ -232,23 +223,36 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// 2^x for two values on the FMA pipe like exp2_poly2 (the same reduction and polynomial), with an
-// exact zero for x = -infinity: a masked key's probability must not be merely small. The exponent is
-// added and kept from going negative in one instruction.
-__device__ __forceinline__ void exp2_poly2_zero(float& y0, float& y1, float x0, float x1) {
-  constexpr float kRound = 12582912.0f;  // 1.5 * 2^23: adding it leaves round(x) in the low mantissa bits
-  constexpr float c0 = 9.999280572e-01f, c1 = 6.932609677e-01f, c2 = 2.426111251e-01f, c3 = 5.517166853e-02f;
-  x0 = fmaxf(x0, -200.0f);
-  x1 = fmaxf(x1, -200.0f);
-  float t0, t1, n0, n1, f0, f1, p0, p1;
-  add2(t0, t1, x0, x1, kRound, kRound);
-  sub2(n0, n1, t0, t1, kRound, kRound);
-  sub2(f0, f1, x0, x1, n0, n1);
-  fma2(p0, p1, c3, c3, f0, f1, c2, c2);
-  fma2(p0, p1, p0, p1, f0, f1, c1, c1);
-  fma2(p0, p1, p0, p1, f0, f1, c0, c0);
-  y0 = __int_as_float(__viaddmax_s32(__float_as_int(p0), __float_as_int(t0) << 23, 0));
-  y1 = __int_as_float(__viaddmax_s32(__float_as_int(p1), __float_as_int(t1) << 23, 0));
+// cap * log2(e) * tanh(x k) of one score, from two results of the special-function unit.
+__device__ __forceinline__ float cap_score(float x, float k, float cap_log2) {
+  return fmaf(-2.f * cap_log2, rcp_approx(1.f + ex2_approx(x * (k * 2.885390081777927f))), cap_log2);
+}
+
+// The same of N scores by an odd polynomial in u = x k, for |u| <= 1/2 (scores stay below their cap by
+// design): off by 2e-7 of the cap (coefficients from unet_latent_attention_b200/fit_tanh_poly.py), in 5
+// packed operations for two values on the FMA pipe; the softmax needs the special-function unit for itself
+// ([2, 10, 4096, 64]: CAPPED us; 332 us with cap_score alone). False, with nothing done, if a score of the
+// warp lies beyond.
+template <int N>
+__device__ __forceinline__ bool cap_small_scores(float (&x)[N], float k, float cap_log2) {
+  float top[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top[e] = max3f(top[e], fabsf(x[i + e]), fabsf(x[i + 4 + e]));
+  if (__any_sync(0xffffffffu, fmaxf(max3f(top[0], top[1], top[2]), top[3]) * k > 0.5f)) return false;
+  const float k2 = k * k, a0 = cap_log2 * k, a1 = a0 * k2, a2 = a1 * k2, a3 = a2 * k2;
+  const float2 c0 = {9.999976754e-01f * a0, 9.999976754e-01f * a0}, c1 = {-3.332065642e-01f * a1, -3.332065642e-01f * a1}, c2 = {1.314514577e-01f * a2, 1.314514577e-01f * a2}, c3 = {-4.337248206e-02f * a3, -4.337248206e-02f * a3};
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 v = make_float2(x[i], x[i + 1]), z = __fmul2_rn(v, v);
+    float2 p = __ffma2_rn(c3, z, c2);
+    p = __ffma2_rn(p, z, c1);
+    p = __ffma2_rn(p, z, c0);
+    p = __fmul2_rn(p, v);
+    x[i] = p.x, x[i + 1] = p.y;
+  }
+  return true;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -276,7 +280,7 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     attention_masked_sm100(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ Params p) {
-  constexpr int BN = C::BN, KS = C::KS, VS = C::VS, HALVES = C::HALVES;
+  constexpr int BN = C::BN, KS = C::KS, VS = C::VS;
   extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's period
   const uint32_t sbase = smem_u32(smem);
   const Bars<KS, VS> bars{sbase + C::BAR_OFF};
@@ -302,11 +306,10 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   if (threadIdx.x == 0) {
     mbar_init(bars.q_full(), 1);
     mbar_init(bars.s_full(), 1);
-    mbar_init(bars.s_free(), 128 * HALVES);
-    mbar_init(bars.p_full(), 128 * HALVES);
+    mbar_init(bars.s_free(), 128);
+    mbar_init(bars.p_full(), 128);
     mbar_init(bars.o_done(), 1);
     mbar_init(bars.fin(), 1);
-    for (int i = 0; i < 4; ++i) mbar_init(bars.halves(i), 2);
     for (int s = 0; s < KS; ++s) {
       mbar_init(bars.k_full(s), 1);
       mbar_init(bars.k_empty(s), 1);
@@ -334,8 +337,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   sd::grid_dep_wait();  // global memory from here on
   sd::grid_dep_launch();
 
-  // Softmax threads: half of the columns (warps 4-7 the first), row of the tile.
-  const int half = HALVES == 2 ? warp >> 3 : 0, r_in = (warp & 3) * 32 + lane;
+  const int r_in = (warp & 3) * 32 + lane;  // softmax threads: the row of the tile
   Row me{0, 0, 0, false};
   if (warp >= 4) {
     const long long r = row0 + r_in;
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 
   if (warp < 4) {
     // ================================================================== helper warps
-    if constexpr (C::CTAS == 2) regs_dec<C::REG_HELPER>();
+    if constexpr (C::CTAS > 1) regs_dec<C::REG_HELPER>();
     const int chunks = (p.dh + 63) / 64;
     if (warp == 0) {
       // ---------------------------------------------------------------- TMA producer
@@ -463,19 +465,40 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     } else if (warp == 2) {
       // ---------------------------------------------------------------- guard
       Ring<VS> rv;
+      constexpr int N = (BM + BN) / 32;
+      float window[N];  // of the next tile: on its way while this one is looked after
+      bool far = false;
+      auto load_window = [&](int j) {
+        const long long d0 = static_cast<long long>(j) * BN - (row0 / p.pack + BM - 1) + shift0;
+        const float* table = p.bias + static_cast<long long>(h0) * (2LL * p.radius + 1) + p.radius;
+        far = is_far(d0, BM + BN - 1, p.radius);
+        if (far) {
+          window[0] = __ldg(table + (d0 >= p.radius ? p.radius : -p.radius));
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) window[i] = __ldg(table + clampll(d0 + i * 32 + lane, -p.radius, p.radius));
+        }
+      };
+      if (C::BIAS && j1 > j0) load_window(j0);
       for (int j = j0; j < j1; ++j) {
         const int s = rv.s;
         if constexpr (C::BIAS) {
           if (j - j0 >= VS && !__all_sync(0xffffffffu, wait_bar(bars.v_empty(s), rv.parity ^ 1, abort_flag, p.err))) break;
-          // Window value e belongs to the distance d0 + e.
-          const long long d0 = static_cast<long long>(j) * BN - (row0 / p.pack + BM - 1) + shift0;
-          const float* table = p.bias + static_cast<long long>(h0) * (2LL * p.radius + 1) + p.radius;
-          float* w = reinterpret_cast<float*>(smem + C::BIAS_OFF) + s * C::WINDOW;
+          // Value e belongs to the distance d0 + e; the copy shifted by c holds it at place e + c.
+          float* w = reinterpret_cast<float*>(smem + C::BIAS_OFF) + s * 4 * C::WINDOW;
+          if (far) {
+            if (lane == 0) w[0] = bias_log2(window[0]);
+          } else {
 #pragma unroll
-          for (int i = 0; i < C::WINDOW / 32; ++i)
-            w[i * 32 + lane] = bias_log2(__ldg(table + clampll(d0 + i * 32 + lane, -p.radius, p.radius)));
+            for (int i = 0; i < N; ++i) {
+              const float y = bias_log2(window[i]);
+#pragma unroll
+              for (int c = 1; c <= 4; ++c) w[(c - 1) * C::WINDOW + c + i * 32 + lane] = y;
+            }
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(bars.bias_full(s));
+          if (j + 1 < j1) load_window(j + 1);
         }
         if (!__all_sync(0xffffffffu, wait_bar(bars.v_full(s), rv.parity, abort_flag, p.err))) break;
         if (j < whole0 || j >= whole1) {
@@ -503,25 +526,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     }
   } else {
     // ================================================================== softmax warps
-    if constexpr (C::CTAS == 2) regs_inc<C::REG_SOFT>();
-    constexpr int HC = C::HC;
+    if constexpr (C::CTAS > 1) regs_inc<C::REG_SOFT>();
     const int quarter = warp & 3;
     const uint32_t tbase = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    const uint32_t tS = tbase + half * HC, tP = tbase + C::TM_P + half * (HC / 2), tO = tbase + C::TM_O;
+    const uint32_t tS = tbase, tP = tbase + C::TM_P, tO = tbase + C::TM_O;
     const bool live = row0 + (r_in & ~31) < rows;  // a warp behind the last row only keeps the barriers going
     const bool is_mixed = C::BIAS && *mixed;
     const int ochunks = (p.dh + 15) / 16;
-    // Exchange with the thread of the row's other half, one phase of the two warps' barrier each time. The
-    // two buffers alternate: a value is overwritten two phases on, after the other warp has read it.
-    volatile float* xch = reinterpret_cast<volatile float*>(smem + C::XCH_OFF) + r_in;
-    auto other_half = [&](float v, int phase, float& theirs) {
-      xch[((phase & 1) * 2 + half) * BM] = v;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars.halves(quarter));
-      const bool met = __all_sync(0xffffffffu, wait_bar(bars.halves(quarter), phase & 1, abort_flag, p.err));
-      theirs = xch[((phase & 1) * 2 + (half ^ 1)) * BM];
-      return met;
-    };
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
     if (!live) {
@@ -545,45 +556,78 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         break;
       }
       tc_fence_after();
-      float sv[HC];
+      float sv[BN];
+      auto load_scores = [&] {
 #pragma unroll
-      for (int c = 0; c < HC / 32; ++c) {
-        uint32_t r[32];
-        tmem_ld32(tS + c * 32, r);
+        for (int c = 0; c < BN / 32; ++c) {
+          uint32_t r[32];
+          tmem_ld32(tS + c * 32, r);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(r[i]);
+          for (int i = 0; i < 32; ++i) sv[c * 32 + i] = __uint_as_float(r[i]);
+        }
+        tmem_wait_ld();
+      };
+      load_scores();
+      // the score is sv * scale + offset, in units of log2
+      float scale = C::CAP ? 1.f : p.scale_log2, offset = 0.f;
+      bool biased = false;
+      if constexpr (C::CAP || C::BIAS) {
+        // The rare forms work on S in tensor memory, 16 columns at a time (a loop that stays out of the
+        // instruction cache's way), in units of log2: large scores under a cap, and a bias over documents
+        // with different shifts, where each row has its own distances.
+        bool slow = is_mixed;
+        if constexpr (C::CAP) slow = slow || !cap_small_scores(sv, p.cap_in, p.cap_out);
+        if (slow) {
+          const float* table = p.bias + static_cast<long long>(h0) * (2LL * p.radius + 1) + p.radius;
+          const long long d = static_cast<long long>(j) * BN - (row0 + r_in) / p.pack + me.shift;
+#pragma unroll 1
+          for (int c = 0; c < BN / 16; ++c) {
+            uint32_t r[16];
+            tmem_ld16(tS + c * 16, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x = __uint_as_float(r[i]);
+              if (C::CAP) x = cap_score(x, p.cap_in, p.cap_out);
+              if (C::BIAS && is_mixed)
+                x = fmaf(x, C::CAP ? 1.f : p.scale_log2, bias_log2(__ldg(table + clampll(d + c * 16 + i, -p.radius, p.radius))));
+              r[i] = __float_as_uint(x);
+            }
+            tmem_st16(tS + c * 16, r);
+          }
+          tmem_wait_st();
+          load_scores();
+          biased = is_mixed;
+          if (is_mixed) scale = 1.f;
+        }
       }
-      tmem_wait_ld();
       if constexpr (C::P_SEP) {
         tc_fence_before();
         mbar_arrive(bars.s_free());
       }
-      if constexpr (C::CAP) {
-        // cap log2(e) tanh(x / cap) = cap log2(e) (1 - 2 / (1 + exp(2 x / cap)))
+      if (C::BIAS && !biased) {
+        const long long d0 = static_cast<long long>(j) * BN - (row0 / p.pack + BM - 1) + shift0;  // the window's first distance
+        const float* w = reinterpret_cast<const float*>(smem + C::BIAS_OFF) + ((j - j0) % VS) * 4 * C::WINDOW;
+        if (is_far(d0, BM + BN - 1, p.radius)) {
+          offset = w[0];
+        } else {
+          // Column i of this row: value e + i, at multiples of four in the copy shifted by c.
+          const int e = BM - 1 - r_in, c = 4 - (e & 3);
+          const float4* mine = reinterpret_cast<const float4*>(w + (c - 1) * C::WINDOW + c + e);
 #pragma unroll
-        for (int i = 0; i < HC; ++i)
-          sv[i] = fmaf(-2.f * p.cap_out, rcp_approx(1.f + ex2_approx(sv[i] * p.cap_in)), p.cap_out);
-      }
-      if constexpr (C::BIAS) {
-        if (!is_mixed) {
-          const float* w = reinterpret_cast<const float*>(smem + C::BIAS_OFF) + ((j - j0) % VS) * C::WINDOW + (BM - 1 - r_in) + half * HC;
-#pragma unroll
-          for (int i = 0; i < HC; ++i) sv[i] = C::CAP ? sv[i] + w[i] : fmaf(sv[i], p.scale_log2, w[i]);
-        } else {  // a tile over documents with different shifts: each row its own distances
-          const float* table = p.bias + static_cast<long long>(h0) * (2LL * p.radius + 1) + p.radius;
-          const long long d0 = static_cast<long long>(j) * BN + half * HC - (row0 + r_in) / p.pack + me.shift;
-#pragma unroll
-          for (int i = 0; i < HC; ++i) {
-            const float y = bias_log2(__ldg(table + clampll(d0 + i, -p.radius, p.radius)));
-            sv[i] = C::CAP ? sv[i] + y : fmaf(sv[i], p.scale_log2, y);
+          for (int i = 0; i < BN; i += 4) {
+            const float4 y = mine[i / 4];
+            fma2(sv[i], sv[i + 1], sv[i], sv[i + 1], scale, scale, y.x, y.y);
+            fma2(sv[i + 2], sv[i + 3], sv[i + 2], sv[i + 3], scale, scale, y.z, y.w);
           }
+          scale = 1.f;
         }
       }
       if (j < whole0 || j >= whole1) {
         // Element masks, 32 columns at a time: a warp's rows mostly see all or nothing of them.
-        const int lo = me.lo - j * BN - half * HC, hi = me.hi - j * BN - half * HC;
+        const int lo = me.lo - j * BN, hi = me.hi - j * BN;
 #pragma unroll
-        for (int w = 0; w < HC / 32; ++w) {
+        for (int w = 0; w < BN / 32; ++w) {
           const int l = min(max(lo - 32 * w, 0), 32), h = min(max(hi - 32 * w, 0), 32);
           const uint32_t seen = static_cast<uint32_t>(((1ull << h) - 1) & ~((1ull << l) - 1));
           if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
@@ -596,39 +640,29 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
       for (int k = 0; k < 8; ++k) pm[k] = sv[k];
 #pragma unroll
-      for (int i = 8; i + 16 <= HC; i += 16)
+      for (int i = 8; i + 16 <= BN; i += 16)
 #pragma unroll
         for (int k = 0; k < 8; ++k) pm[k] = max3f(pm[k], sv[i + k], sv[i + 8 + k]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], sv[HC - 8 + k]);
-      float mx = max3f(max3f(pm[0], pm[1], pm[2]), max3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])), theirs;
-      if constexpr (HALVES == 2) {
-        if (!other_half(mx, j - j0, theirs)) {
-          ok = false;
-          break;
-        }
-        mx = fmaxf(mx, theirs);
-      }
-      constexpr bool kLog2 = C::CAP || C::BIAS;  // sv is in units of log2 already
-      const float m_new = fmaxf(m_run, kLog2 ? mx : mx * p.scale_log2);
+      for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], sv[BN - 8 + k]);
+      const float mx = max3f(max3f(pm[0], pm[1], pm[2]), max3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+      // A row without a seen key keeps m = -infinity whatever the offset is.
+      const float m_new = fmaxf(m_run, C::BIAS ? (mx == -INFINITY ? mx : fmaf(mx, scale, offset)) : mx * scale);
       // Row by row: no row's bits depend on its neighbours' scores.
       const bool raise = m_new > m_run + 8.0f, rescale = __any_sync(0xffffffffu, raise);
       const float alpha = !raise ? 1.0f : m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
       if (raise) m_run = m_new;
-      const float neg_m = m_run == -INFINITY ? 0.f : -m_run;  // a row that has seen nothing: all its exp2 are 0
-      uint32_t pk[HC / 2];
+      // exp2(scale sv + offset - m); a row that has seen nothing gets zeros
+      const float minus_m = (m_run == -INFINITY ? 0.f : -m_run) + (C::BIAS ? offset : 0.f);
+      uint32_t pk[BN / 2];
       float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
 #pragma unroll
-      for (int i = 0; i < HC / 2; ++i) {
+      for (int i = 0; i < BN / 2; ++i) {
         float x0, x1;
-        if constexpr (kLog2) add2(x0, x1, sv[2 * i], sv[2 * i + 1], neg_m, neg_m);
-        else fma2(x0, x1, sv[2 * i], sv[2 * i + 1], p.scale_log2, p.scale_log2, neg_m, neg_m);
-        if ((i & 7) < C::POLY) {
-          exp2_poly2_zero(x0, x1, x0, x1);
-        } else {
-          x0 = ex2_approx(x0);
-          x1 = ex2_approx(x1);
-        }
+        if constexpr (C::CAP && !C::BIAS) add2(x0, x1, sv[2 * i], sv[2 * i + 1], minus_m, minus_m);
+        else fma2(x0, x1, sv[2 * i], sv[2 * i + 1], scale, scale, minus_m, minus_m);
+        x0 = ex2_approx(x0);
+        x1 = ex2_approx(x1);
         if (i & 1) add2(ls2, ls3, ls2, ls3, x0, x1);
         else add2(ls0, ls1, ls0, ls1, x0, x1);
         pk[i] = C::F16 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
@@ -640,8 +674,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           break;
         }
         tc_fence_after();
-        if (rescale) {  // the two halves take every other 16 columns of O
-          for (int c = half; c < ochunks; c += HALVES) {
+        if (rescale) {
+          for (int c = 0; c < ochunks; ++c) {
             uint32_t r[16];
             tmem_ld16(tO + c * 16, r);
             tmem_wait_ld();
@@ -652,7 +686,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
       }
 #pragma unroll
-      for (int c = 0; c < HC / 32; ++c) {
+      for (int c = 0; c < BN / 32; ++c) {
         uint32_t r[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) r[i] = pk[c * 16 + i];
@@ -664,12 +698,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     }
     if (ok && j1 > j0) ok = __all_sync(0xffffffffu, wait_bar(bars.o_done(), (j1 - j0 - 1) & 1, abort_flag, p.err));
     tc_fence_after();
-    if (HALVES == 2 && live && ok && j1 > j0) {
-      float theirs;
-      ok = other_half(l_run, j1 - j0, theirs);
-      l_run = half ? theirs + l_run : l_run + theirs;
-    }
-    // ------------------------------------------------------------------ epilogue: every other 16 columns of a row
+    // ------------------------------------------------------------------ epilogue: one row a thread
     const long long row = row0 + r_in;
     const int i_q = static_cast<int>(row / p.pack), h = h0 + static_cast<int>(row % p.pack);
     // Values that the guard set to zero, for rows that see them: 16 columns from c16 of the masked tiles.
@@ -698,7 +727,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.o_batch + i_q * p.o_token + h * p.o_head;
     const float inv = join ? 1.f : l_run == 0.f ? 0.f : 1.0f / l_run;
     if (live) {
-      for (int c = half; c < ochunks; c += HALVES) {
+      for (int c = 0; c < ochunks; ++c) {
         float o[16];
         if (has_o) {  // warp-wide: every lane takes part
           uint32_t r[16];
@@ -726,7 +755,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           if (c * 16 + 8 < p.dh) dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
         }
       }
-      if (join && store && half == 0) {
+      if (join && store) {
         part[C::DHT] = m_run;
         part[C::DHT + 1] = l_run;
       }

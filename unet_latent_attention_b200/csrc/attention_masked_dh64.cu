@@ -1,10 +1,6 @@
 // sd_attention_masked for heads of up to 64 columns.
 #include "attention_masked_launch.cuh"
 
-#ifndef V
-#define V 2, 2, 2
-#define VSEP true
-#endif
 sd_status sd::masked::launch_dh64(const Launch& l) {
-  return l.args->dtype ? by_score<64, 128, V, VSEP, true>(l) : by_score<64, 128, V, VSEP, false>(l);
+  return l.args->dtype ? by_score<64, 128, 2, 2, 2, true, true>(l) : by_score<64, 128, 2, 2, 2, true, false>(l);
 }

@@ -43,7 +43,7 @@ sd_status launch(const Launch& l, int pack, int64_t tiles, int splits) {
                       : 1;
   constexpr float kLog2e = 1.4426950408889634f;
   p.scale_log2 = std::max(a.scale * kLog2e, 1.17549435e-38f);  // scale 0: a masked score must not become 0 * -infinity
-  p.cap_in = C::CAP ? 2.f * kLog2e * (a.scale / a.cap) : 0.f;
+  p.cap_in = C::CAP ? a.scale / a.cap : 0.f;
   p.cap_out = a.cap * kLog2e;
   p.err = sd::device_status_word();
   if (!p.err) return SD_ERR_CUDA;
