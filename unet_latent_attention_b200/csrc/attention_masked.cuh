@@ -54,7 +54,7 @@ struct Params {
   long long o_batch, o_token, o_head;  // strides in elements
   long long v_batch, v_token, v_head;
   int heads, group;      // query heads; query heads per key head
-  int pack;              // heads that are rows of one tile (1 or group)
+  int pack, pack_log2;   // heads that are rows of one tile (1 or group, a power of two)
   int Lq, Lk, dh, docs, radius, causal;
   int tiles;             // query tiles of a plane (one batch's packed head)
   int planes, plane_group;  // planes; planes whose items are mixed
@@ -302,6 +302,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   const int b = plane / heads_packed, h0 = plane % heads_packed * p.pack, kvh = h0 / p.group;
   const long long rows = static_cast<long long>(p.Lq) * p.pack;    // of this (batch, packed head)
   const long long row0 = static_cast<long long>(qt) * BM;
+  const int q_first = static_cast<int>(row0 >> p.pack_log2);  // the first row's query
 
   if (threadIdx.x == 0) {
     mbar_init(bars.q_full(), 1);
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   if (warp >= 4) {
     const long long r = row0 + r_in;
     if (r < rows) {
-      me = row_of(p, b, static_cast<int>(r / p.pack));
+      me = row_of(p, b, static_cast<int>(r >> p.pack_log2));
       if (r_in == 0) bounds->lo_first = me.lo, bounds->hi_first = me.hi;
       if (r_in == BM - 1 || r == rows - 1) bounds->lo_last = me.lo, bounds->hi_last = me.hi;
     }
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
   long long shift0 = 0;
   if constexpr (C::BIAS) {
     // The window of distances assumes one shift for the tile's rows; documents may differ in theirs.
-    shift0 = row_of(p, b, static_cast<int>(row0 / p.pack)).shift;
+    shift0 = row_of(p, b, static_cast<int>(row0 >> p.pack_log2)).shift;
     if (me.exists && me.hi > me.lo && me.shift != shift0) *mixed = 1;
     __syncthreads();
   }
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       if (lane == 0 && j1 > j0) {
         mbar_arrive_expect_tx(bars.q_full(), chunks * BM * 128);
         for (int c = 0; c < chunks; ++c)
-          tma_load_4d(sbase + c * BM * 128, &tm_q, bars.q_full(), c * 64, h0, static_cast<int>(row0 / p.pack), b);
+          tma_load_4d(sbase + c * BM * 128, &tm_q, bars.q_full(), c * 64, h0, static_cast<int>(row0 >> p.pack_log2), b);
         Ring<KS> rk;
         Ring<VS> rv;
         int nk = 0, nv = 0;  // tiles issued
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       float window[N];  // of the next tile: on its way while this one is looked after
       bool far = false;
       auto load_window = [&](int j) {
-        const long long d0 = static_cast<long long>(j) * BN - (row0 / p.pack + BM - 1) + shift0;
+        const long long d0 = static_cast<long long>(j) * BN - (q_first + BM - 1) + shift0;
         const float* table = p.bias + static_cast<long long>(h0) * (2LL * p.radius + 1) + p.radius;
         far = is_far(d0, BM + BN - 1, p.radius);
         if (far) {
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         if constexpr (C::CAP) slow = slow || !cap_small_scores(sv, p.cap_in, p.cap_out);
         if (slow) {
           const float* table = p.bias + static_cast<long long>(h0) * (2LL * p.radius + 1) + p.radius;
-          const long long d = static_cast<long long>(j) * BN - (row0 + r_in) / p.pack + me.shift;
+          const long long d = static_cast<long long>(j) * BN - (q_first + r_in) + me.shift;
 #pragma unroll 1
           for (int c = 0; c < BN / 16; ++c) {
             uint32_t r[16];
@@ -606,7 +607,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         mbar_arrive(bars.s_free());
       }
       if (C::BIAS && !biased) {
-        const long long d0 = static_cast<long long>(j) * BN - (row0 / p.pack + BM - 1) + shift0;  // the window's first distance
+        const long long d0 = static_cast<long long>(j) * BN - (q_first + BM - 1) + shift0;  // the window's first distance
         const float* w = reinterpret_cast<const float*>(smem + C::BIAS_OFF) + ((j - j0) % VS) * 4 * C::WINDOW;
         if (is_far(d0, BM + BN - 1, p.radius)) {
           offset = w[0];
@@ -700,7 +701,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     tc_fence_after();
     // ------------------------------------------------------------------ epilogue: one row a thread
     const long long row = row0 + r_in;
-    const int i_q = static_cast<int>(row / p.pack), h = h0 + static_cast<int>(row % p.pack);
+    const int i_q = static_cast<int>(row >> p.pack_log2), h = h0 + static_cast<int>(row & (p.pack - 1));
     // Values that the guard set to zero, for rows that see them: 16 columns from c16 of the masked tiles.
     auto add_cleaned = [&](int c16, float (&o)[16]) {
       const uint16_t* v = p.v + b * p.v_batch + kvh * p.v_head + c16;
@@ -776,7 +777,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       for (int w = rank * C::THREADS + static_cast<int>(threadIdx.x); w < live_rows * groups; w += splits * C::THREADS) {
         const int r = w / groups, c = w % groups * 8;
         const long long at = row0 + r;
-        if (!row_of(p, b, static_cast<int>(at / p.pack)).exists) continue;
+        if (!row_of(p, b, static_cast<int>(at >> p.pack_log2)).exists) continue;
         float m = -INFINITY;
         for (int k = 0; k < splits; ++k) m = fmaxf(m, peer_load4(sbase + (r * C::JOIN_ROW + C::DHT) * 4, k).x);
         float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -795,7 +796,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           q[i] = C::F16 ? pack_f16x2(o[2 * i] * inv, o[2 * i + 1] * inv) : pack_bf16x2(o[2 * i] * inv, o[2 * i + 1] * inv);
-        uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.o_batch + (at / p.pack) * p.o_token + (h0 + at % p.pack) * p.o_head;
+        uint16_t* out = static_cast<uint16_t*>(p.out) + b * p.o_batch + (at >> p.pack_log2) * p.o_token + (h0 + (at & (p.pack - 1))) * p.o_head;
         *reinterpret_cast<uint4*>(out + c) = make_uint4(q[0], q[1], q[2], q[3]);
       }
     cluster_sync();  // no CTA leaves while a peer reads its part

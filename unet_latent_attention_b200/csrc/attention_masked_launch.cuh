@@ -31,6 +31,7 @@ sd_status launch(const Launch& l, int pack, int64_t tiles, int splits) {
   p.o_batch = a.o_stride[0], p.o_token = a.o_stride[1], p.o_head = a.o_stride[2];
   p.v_batch = a.v_stride[0], p.v_token = a.v_stride[1], p.v_head = a.v_stride[2];
   p.heads = static_cast<int>(a.heads), p.group = static_cast<int>(l.group), p.pack = pack;
+  while (1 << p.pack_log2 < pack) ++p.pack_log2;
   p.Lq = static_cast<int>(a.Lq), p.Lk = static_cast<int>(a.Lk), p.dh = static_cast<int>(a.dh);
   p.docs = a.q_offsets ? static_cast<int>(a.docs) : 0;
   p.radius = static_cast<int>(a.bias_radius), p.causal = a.causal;
