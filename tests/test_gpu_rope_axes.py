@@ -81,6 +81,30 @@ def test_many_rows_take_four_heads_a_thread(cuda):
     assert torch.equal(qs, qo[:, :16]) and torch.equal(ks, ko[:, :16])
 
 
+@pytest.mark.parametrize("H,KV", [(1, 1), (2, 2), (3, 1), (1, 0), (4, 3), (8, 1), (1, 6), (40, 10)])
+@pytest.mark.parametrize("dh", [16, 64, 128, 160])
+def test_every_head_of_many_tokens_is_written(cuda, dh, H, KV):
+    # however the heads are dealt to the threads: every value, against the rotation in torch's fp64
+    axes = (dh // 2, dh // 2)
+    L = 12001
+    q, k, pos, (wq, wk) = _inputs(1, L, H, max(KV, 1), dh, torch.float16, 60 + dh + H, cuda, axes)
+    freqs = sdk.rope_frequencies(axes)
+    for norm in (False, True):
+        qo, ko = (torch.full_like(x, float("nan")) for x in (q, k))
+        sdk.sd_rope_axes(q, k if KV else None, pos, freqs, axes, q_weight=wq if norm else None, k_weight=wk if norm else None,
+                         q_out=qo, k_out=ko if KV else None)
+        for x, y, w in ((q, qo, wq), (k, ko, wk))[:2 if KV else 1]:
+            axis = torch.tensor([a for a, d in enumerate(axes) for _ in range(d // 2)], device=cuda)
+            angle = 2 * np.pi * (pos.double()[..., axis] * (freqs.double() * 2.0 ** -64))[:, :, None]
+            n = x.double()
+            if norm:
+                n = n / (n.pow(2).mean(-1, keepdim=True) + 1e-6).sqrt() * w.double()
+            a, b = n[..., 0::2], n[..., 1::2]
+            ref = torch.stack((a * angle.cos() - b * angle.sin(), a * angle.sin() + b * angle.cos()), -1).flatten(-2)
+            tol = ref.abs() * 2.0 ** -11 + 2e-6 * n.abs().amax(-1, keepdim=True) + 2.0 ** -24
+            assert ((y.double() - ref).abs() <= tol).all()
+
+
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_fused_projection_in_place_and_layouts(cuda, dtype):
     t, axes, half = TYPES[dtype], (16, 24, 24), True

@@ -2,7 +2,6 @@
 #pragma once
 
 #include <algorithm>
-#include <cstdlib>
 #include <atomic>
 
 #include "attention_masked.cuh"
@@ -92,7 +91,6 @@ sd_status choose(const Launch& l) {
   int splits = 1;
   const int64_t key_tiles = (a.Lk + C::BN - 1) / C::BN;
   while (2 * splits <= kMaxSplits && planes * tiles * 2 * splits <= C::CTAS * sd::sm_count() && key_tiles >= 4 * splits) splits *= 2;
-  if (const char* e = getenv("SPLITS")) splits = atoi(e);
   return launch<C>(l, pack, tiles, splits);
 }
 

@@ -296,7 +296,8 @@ sd_status by_heads(const RopeKernelArgs& a, int64_t tokens, cudaStream_t s) {
   const int rows = (heads * per + kTeams - 1) / kTeams;  // heads of a team
   auto pick = [&](auto norm) {
     constexpr bool N = decltype(norm)::value;
-    if (rows >= 8) return launch<T, HALF, LANES, N, 4, true>(a, tokens, per, s);
+    // (a token with one team has no other for k)
+    if (rows >= 8 || kTeams / per == 1) return launch<T, HALF, LANES, N, 4, true>(a, tokens, per, s);
     if (rows >= 4) return launch<T, HALF, LANES, N, 2, false>(a, tokens, per, s);
     return launch<T, HALF, LANES, N, 1, false>(a, tokens, per, s);
   };
