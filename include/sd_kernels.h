@@ -335,7 +335,7 @@ sd_status sd_rope_axes(const sd_rope_args* args, void* stream);
  *           h / (heads / kv_heads); kv_heads divides heads. o must not overlap q, k or v, nor fold
  *           onto itself.
  *  dh     : a multiple of 8 from 8 to 160.  Lq, Lk < 2^30, B * heads < 2^31. Lk = 0 gives zeros.
- *  scale  : finite and >= 0.  cap: 0 = none, else in [1e-6, 1e30].
+ *  scale  : finite and >= 0.  cap: 0 = none, else in [1e-6, 1e30], with scale / cap below 1e5.
  *  bias   : fp32 [heads, 2 * bias_radius + 1] or NULL; 0 <= bias_radius < 2^29. Values may be
  *           -infinity, or the lowest of a type; +infinity and NaN spread over their rows.
  *  causal : 0 or 1.  kv_lens, q_starts, prefix_lens: int32, one per sequence, or NULL (prefix 0).

@@ -299,3 +299,25 @@ def test_overlap_is_refused(cuda):
         sdk.sd_attention_masked(big[:2], big[:2], big[:2], out=big[1:])
     with pytest.raises(sdk.SDError, match="heads overlap"):
         sdk.sd_attention_masked(big[:2], big[:2], big[:2], out=torch.zeros(4, 1, 128, 64, dtype=torch.bfloat16, device=cuda).as_strided((2, 2, 128, 64), (8192, 64, 64, 1)))
+
+
+def test_few_queries_of_documents_split_over_a_cluster(cuda):
+    # queries of three documents (one of them with no key) in one tile, against long keys
+    q, k, v = _tensors(1, 4, 2, 90, 3000, 64, torch.bfloat16, 97, cuda, True)
+    off = dict(q_offsets=_ints([2, 30, 31, 80], cuda), k_offsets=_ints([0, 1100, 1100, 2990], cuda))
+    for kw in (dict(), dict(causal=True), dict(causal=True, q_starts=_ints([500, 0, -20], cuda)), dict(bias=_bias(4, 60, 98, cuda), cap=9.0)):
+        out = torch.full_like(q, 7.0)
+        kw = dict(kw, **off)
+        o = sdk.sd_attention_masked(q, k, v, layout="blhd", out=out, **kw)
+        _check(o, q, k, v, "blhd", out=torch.full_like(q, 7.0), **kw)
+
+
+@pytest.mark.parametrize("cap", [1e-6, 0.3, 1e30])
+def test_extreme_caps(cuda, cap):
+    q, k, v = _tensors(1, 2, 2, 150, 200, 64, torch.bfloat16, 99, cuda)
+    q[:, :, 5] = 0  # scores of exactly zero
+    _check(sdk.sd_attention_masked(q, k, v, cap=cap), q, k, v, cap=cap)
+    with pytest.raises(sdk.SDError, match="cap"):
+        sdk.sd_attention_masked(q, k, v, scale=1.0, cap=1e-7)
+    with pytest.raises(sdk.SDError, match="cap"):
+        sdk.sd_attention_masked(q, k, v, scale=1e30, cap=1.0)

@@ -78,8 +78,11 @@ extern "C" sd_status sd_attention_masked(const sd_attention_masked_args* args, v
   if (!std::isfinite(a.scale) || !std::isfinite(a.cap) || a.cap < 0.f)
     return sd::fail(SD_ERR_INVALID_ARG, "sd_attention_masked: scale must be finite, cap finite and >= 0");
   if (a.scale < 0.f) return sd::fail(SD_ERR_UNSUPPORTED, "sd_attention_masked: negative scale");
-  if (a.cap > 0.f && !(a.cap >= 1e-6f && a.cap <= 1e30f && a.scale / a.cap <= 1e30f))
-    return sd::fail(SD_ERR_UNSUPPORTED, "sd_attention_masked: cap must lie in [1e-6, 1e30]");
+  if (a.cap > 0.f) {  // the cap's polynomial has coefficients up to cap * (scale / cap)^7
+    const float k = a.scale / a.cap, top = 1.5f * a.cap * k * k * k * k * k * k * k;
+    if (!(a.cap >= 1e-6f && a.cap <= 1e30f) || !std::isfinite(k * k * k * k * k * k) || !std::isfinite(top))
+      return sd::fail(SD_ERR_UNSUPPORTED, "sd_attention_masked: cap must lie in [1e-6, 1e30], scale / cap below 1e5");
+  }
   if (a.bias && (a.bias_radius < 0 || a.bias_radius >= (int64_t(1) << 29)))
     return sd::fail(SD_ERR_INVALID_ARG, "sd_attention_masked: bias_radius must lie in [0, 2^29)");
   if (a.prefix_lens && !a.causal) return sd::fail(SD_ERR_INVALID_ARG, "sd_attention_masked: prefix_lens needs causal");

@@ -8,21 +8,31 @@
 // row to hi of its last one, and only those that reach past lo of the last or hi of the first row need
 // element masks: the others run as if there were no mask.
 //
-// A CTA owns NQ tiles of 128 query rows of one (batch, head) and streams the key tiles of both once.
-//  * warp 0: TMA producer of Q and of the K/V ring (rows past the end read as zeros).
-//  * warps 1, 2: one thread each issues the tcgen05 work of one query tile: S = Q K^T into tensor
-//    memory, O += P V with P read from tensor memory. Up to 64 columns P has columns of its own, so
-//    the next S runs while this one is in its softmax; above, P lies over S (two tiles' S and O fill
-//    tensor memory) and the other tile's work fills the wait.
-//  * warp 3: the guard. It waits for every V tile and, where the tile has masked elements, sets its
+// A CTA of 256 threads owns 128 query rows of one (batch, head) and streams their key tiles:
+//  * warp 0: TMA producer of Q and of the rings of key and value tiles (rows past the end read as
+//    zeros). The rings are apart: a key tile is free once S = Q K^T is done, a value tile only after P V.
+//  * warp 1 issues the tcgen05 work: S = Q K^T into tensor memory, O += P V with P read from tensor
+//    memory. P has columns of its own, so the next S runs while this one is in its softmax.
+//  * warp 2: the guard. It waits for every V tile and, where the tile has masked elements, sets its
 //    infinities and NaN to zero: a zero probability times them would be NaN in rows that do not see
-//    them. (Rows that do see one add it in the epilogue.) With a bias it also copies the 383 values
-//    that the tile's distances can take into shared memory.
-//  * four warps per query tile: one row a thread, fp32 maximum and sum, exp2, P rounded to the
-//    input's type. The running maximum is raised only when it grows by more than 2^8.
+//    them. (Rows that do see one add it in the epilogue.) With a bias it also copies the values that
+//    the tile's distances can take into shared memory.
+//  * warps 4-7: one row a thread, fp32 maximum and sum, exp2, P rounded to the input's type. The
+//    running maximum is raised only when it grows by more than 2^8.
+// Two CTAs share an SM (up to 128 columns): while one waits for S, P V or a copy, the other has the
+// special-function unit, and one's start and end hide behind the other's tiles. No waiting is shared
+// between them, so items of any length mix. (Two query tiles in one CTA, with turns on the
+// special-function unit, took 192 us where this takes 150 for [2, 10, 4096, 64], and 187 where this takes 140 for [2, 8, 4096,
+// 128]; eight softmax warps on half rows 193 and 164 with one CTA, 160 with two at 64 columns.)
+//
 // Few query rows: the CTAs of a cluster take equal parts of the key tiles and join (m, l, O) through
 // distributed shared memory in rank order, so the result does not depend on timing and no workspace
 // is needed. Heads that share a key head are rows of the same tile then.
+//
+// What bounds it (B200, cycles of a softmax warp per 128 keys, two CTAs, 64 columns, no bias or cap): exp2
+// 1400 of 2800, where the special-function unit alone needs 1024 for one CTA's tile; 440 waiting for S, 560 for
+// maxima, masks and copies. Of 2 * 16 * 10 * 2 query tiles 296 run at a time, so a call of few waves
+// also waits for its last one.
 //
 // All waits on mbarriers are bounded; see attn_common.cuh.
 #pragma once
@@ -116,10 +126,10 @@ __device__ inline Row row_of(const Params& p, int b, int i) {
 
 // DHT: padded head size (64-column chunks of shared memory; N of O is dh rounded up to 16). BN: keys of
 // a tile. KS, VS: stages of the rings of key and value tiles. CTAS: CTAs of an SM.
-template <int DHT_, int BN_, int KS_, int VS_, int CTAS_, bool P_SEP_, bool F16_, bool CAP_, bool BIAS_>
+template <int DHT_, int BN_, int KS_, int VS_, int CTAS_, bool F16_, bool CAP_, bool BIAS_>
 struct Cfg {
   static constexpr int DHT = DHT_, BN = BN_, KS = KS_, VS = VS_, CTAS = CTAS_;
-  static constexpr bool P_SEP = P_SEP_, F16 = F16_, CAP = CAP_, BIAS = BIAS_;
+  static constexpr bool F16 = F16_, CAP = CAP_, BIAS = BIAS_;
   static constexpr int NCH = (DHT + 63) / 64;
   static constexpr int Q_TILE = NCH * BM * 128, KV_TILE = NCH * BN * 128;
   static constexpr int K_OFF = Q_TILE, V_OFF = K_OFF + KS * KV_TILE;
@@ -135,8 +145,8 @@ struct Cfg {
   static constexpr int MISC_OFF = BAR_OFF + NBARS * 8;  // TMEM address, abort flag, cleaned flag, mixed flag
   static constexpr int BOUNDS_OFF = MISC_OFF + 16;      // lo of the first and last row, hi of both
   static constexpr int SMEM = BOUNDS_OFF + 16;
-  static constexpr int TM_P = P_SEP ? BN : 0, TM_O = P_SEP ? BN + BN / 2 : BN;
-  static constexpr int TM_COLS = TM_O + DHT <= 128 ? 128 : TM_O + DHT <= 256 ? 256 : 512;
+  static constexpr int TM_P = BN, TM_O = BN + BN / 2;  // tensor memory columns: S | P | O
+  static constexpr int TM_COLS = TM_O + DHT <= 256 ? 256 : 512;
   static constexpr int THREADS = 256;
   static constexpr int REG_HELPER = 64, REG_SOFT = 192;  // two CTAs an SM: registers move to the softmax warps
   // Join of a cluster's parts: rows of DHT fp32 and (m, l), over Q and the rings.
@@ -231,7 +241,7 @@ __device__ __forceinline__ float cap_score(float x, float k, float cap_log2) {
 // The same of N scores by an odd polynomial in u = x k, for |u| <= 1/2 (scores stay below their cap by
 // design): off by 2e-7 of the cap (coefficients from unet_latent_attention_b200/fit_tanh_poly.py), in 5
 // packed operations for two values on the FMA pipe; the softmax needs the special-function unit for itself
-// ([2, 10, 4096, 64]: CAPPED us; 332 us with cap_score alone). False, with nothing done, if a score of the
+// ([2, 10, 4096, 64]: 226 us; 332 us with cap_score alone). False, with nothing done, if a score of the
 // warp lies beyond.
 template <int N>
 __device__ __forceinline__ bool cap_small_scores(float (&x)[N], float k, float cap_log2) {
@@ -439,8 +449,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         }
         __syncwarp();
       };
-      // S of the next tile is issued before P V of this one, as soon as S has been read; where P lies
-      // over S, once P V is complete.
+      // S of the next tile is issued before P V of this one, as soon as S has been read.
       bool ok = j1 <= j0 || wait(bars.q_full(), 0);
       Ring<KS> rk;
       Ring<VS> rv;
@@ -452,12 +461,11 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       };
       int n = 0;
       for (int j = j0; ok && j < j1; ++j, ++n) {
-        if (!C::P_SEP && n > 0 && !(ok = finish(n - 1))) break;
         if (!(ok = wait(bars.k_full(rk.s), rk.parity))) break;
-        if (n > 0 && !(ok = wait(C::P_SEP ? bars.s_free() : bars.o_done(), (n - 1) & 1))) break;
+        if (n > 0 && !(ok = wait(bars.s_free(), (n - 1) & 1))) break;
         issue_qk(rk.s);
         rk.next();
-        if (C::P_SEP && n > 0 && !(ok = finish(n - 1))) break;
+        if (n > 0 && !(ok = finish(n - 1))) break;
       }
       if (ok && n > 0) finish(n - 1);
       if (elect_one()) mma_commit(bars.fin());
@@ -540,7 +548,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       for (int j = j0; ok && j < j1; ++j) {
         const int par = (j - j0) & 1;
         ok = __all_sync(0xffffffffu, wait_bar(bars.s_full(), par, abort_flag, p.err));
-        if (ok && C::P_SEP) mbar_arrive(bars.s_free());
+        if (ok) mbar_arrive(bars.s_free());
         // as the other warps: no arrival for this P before every warp's for the one before it
         if (ok && j > j0) ok = __all_sync(0xffffffffu, wait_bar(bars.o_done(), par ^ 1, abort_flag, p.err));
         if (ok) mbar_arrive(bars.p_full());
@@ -602,10 +610,8 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           if (is_mixed) scale = 1.f;
         }
       }
-      if constexpr (C::P_SEP) {
-        tc_fence_before();
-        mbar_arrive(bars.s_free());
-      }
+      tc_fence_before();
+      mbar_arrive(bars.s_free());
       if (C::BIAS && !biased) {
         const long long d0 = static_cast<long long>(j) * BN - (q_first + BM - 1) + shift0;  // the window's first distance
         const float* w = reinterpret_cast<const float*>(smem + C::BIAS_OFF) + ((j - j0) % VS) * 4 * C::WINDOW;

@@ -36,7 +36,8 @@ sd_status launch(const Launch& l, int pack, int64_t tiles, int splits) {
   p.radius = static_cast<int>(a.bias_radius), p.causal = a.causal;
   p.tiles = static_cast<int>(tiles);
   p.planes = static_cast<int>(a.B * (a.heads / pack));
-  // Where items differ in length, as many planes are mixed as have 48 MB of keys and values (half of L2).
+  // Where items differ in length, as many planes are mixed as have 48 MB of keys and values, under half of
+  // L2 (causal [2, 10, 4096, 64]: 77 us with all 20 planes mixed, 106 one after the other).
   const int64_t plane_bytes = std::max<int64_t>(a.Lk * a.dh * 4 * pack / l.group, 1);
   p.plane_group = a.causal || a.q_offsets || a.kv_lens
                       ? static_cast<int>(std::min<int64_t>(std::max<int64_t>((int64_t(48) << 20) / plane_bytes, 1), p.planes))
@@ -87,20 +88,22 @@ sd_status choose(const Launch& l) {
   int pack = 1;
   if (!C::BIAS && a.Lq <= BM / 2 && l.group > 1 && BM % l.group == 0) pack = static_cast<int>(l.group);
   const int64_t planes = a.B * (a.heads / pack), tiles = (a.Lq * pack + BM - 1) / BM;
-  // Idle SMs: split the keys over a cluster, two key tiles a CTA at least.
+  // Idle SMs: split the keys over a cluster, two key tiles a CTA at least, while all clusters run at once.
+  // (Beyond that the clusters' starts, joins and ends cost more than they even out: B200, [32, 16, 1, 2048
+  // ragged, 64] takes 52, 61, 91 and 167 us with 1, 2, 4 and 8 parts; [4, 32 / 8 heads, 1, 16384, 128] 232, 122, 68 and 49.)
   int splits = 1;
   const int64_t key_tiles = (a.Lk + C::BN - 1) / C::BN;
   while (2 * splits <= kMaxSplits && planes * tiles * 2 * splits <= C::CTAS * sd::sm_count() && key_tiles >= 4 * splits) splits *= 2;
   return launch<C>(l, pack, tiles, splits);
 }
 
-template <int DHT, int BN, int KS, int VS, int CTAS, bool P_SEP, bool F16>
+template <int DHT, int BN, int KS, int VS, int CTAS, bool F16>
 sd_status by_score(const Launch& l) {
   const bool cap = l.args->cap != 0.f, bias = l.args->bias != nullptr;
-  if (cap && bias) return choose<Cfg<DHT, BN, KS, VS, CTAS, P_SEP, F16, true, true>>(l);
-  if (cap) return choose<Cfg<DHT, BN, KS, VS, CTAS, P_SEP, F16, true, false>>(l);
-  if (bias) return choose<Cfg<DHT, BN, KS, VS, CTAS, P_SEP, F16, false, true>>(l);
-  return choose<Cfg<DHT, BN, KS, VS, CTAS, P_SEP, F16, false, false>>(l);
+  if (cap && bias) return choose<Cfg<DHT, BN, KS, VS, CTAS, F16, true, true>>(l);
+  if (cap) return choose<Cfg<DHT, BN, KS, VS, CTAS, F16, true, false>>(l);
+  if (bias) return choose<Cfg<DHT, BN, KS, VS, CTAS, F16, false, true>>(l);
+  return choose<Cfg<DHT, BN, KS, VS, CTAS, F16, false, false>>(l);
 }
 
 }  // namespace masked
