@@ -415,11 +415,12 @@ def sd_rms_norm_fp8(x, weight=None, eps: float = 1e-6, residual=None, block: int
     C = x.shape[-1]
     shape = (*x.shape[:-1], -(-C // block) if block else 1)
     if out is None:
-        out = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        out = (torch.empty_like(x, dtype=torch.float8_e4m3fn) if x.is_contiguous()
+               else x.new_empty(x.shape, dtype=torch.float8_e4m3fn))
     elif out.shape != x.shape or out.dtype != torch.float8_e4m3fn:
         raise ValueError("out must have the shape of x and type float8_e4m3fn")
     if scales is None:
-        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+        scales = x.new_empty(shape, dtype=torch.float32)
     elif scales.shape != shape or scales.dtype != torch.float32 or not scales.is_contiguous():
         raise ValueError(f"scales must be contiguous fp32 {list(shape)}")
     ro = _rms("sd_rms_norm_fp8", x, weight, float(eps), residual, out, residual_out, scales, block)

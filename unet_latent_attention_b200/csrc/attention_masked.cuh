@@ -148,7 +148,7 @@ struct Cfg {
   static constexpr int TM_P = BN, TM_O = BN + BN / 2;  // tensor memory columns: S | P | O
   static constexpr int TM_COLS = TM_O + DHT <= 256 ? 256 : 512;
   static constexpr int THREADS = 256;
-  static constexpr int REG_HELPER = 64, REG_SOFT = 192;  // two CTAs an SM: registers move to the softmax warps
+  static constexpr int REG_HELPER = 48, REG_SOFT = 208;  // two CTAs an SM: registers move to the softmax warps
   // Join of a cluster's parts: rows of DHT fp32 and (m, l), over Q and the rings.
   static constexpr int JOIN_ROW = DHT + 4;  // floats a row (+4: rows start in different banks)
   static_assert(CTAS * TM_COLS <= 512 && CTAS * (SMEM + 1024) <= 228 * 1024, "on-chip memory");
