@@ -243,7 +243,8 @@ sd_status sd_cfg_dpmpp_3m_step(const float* x, const float* eps_u, const float* 
  * RMS norm of rows with the residual's addition: for each of `rows` rows of `cols` values
  *   h = x + residual (x where residual is NULL), in fp32,
  *   residual_out = h rounded to the type,   y = h * rsqrt(mean(h^2) + eps) * weight
- * y is formed from the unrounded h and rounded once.
+ * y is formed from the unrounded h and rounded once. Squares are summed in fp32 (magnitudes above 1e19
+ * overflow them).
  *  dtype  : of x, residual, residual_out and y: 0 = bf16, 1 = fp16, 2 = fp32.
  *  weight : [cols], fp32 (weight_f32 = 1) or of the type dtype (weight_f32 = 0); NULL = ones.
  *  residual, residual_out : may be NULL; residual_out needs residual.
@@ -322,7 +323,8 @@ sd_status sd_rope_axes(const sd_rope_args* args, void* stream);
  *   key j is seen if j < len_s and (not causal, or j <= p, or j < prefix_s);
  *   o_i = sum_j softmax_j(t_ij over the seen keys) v_j, and 0 where no key is seen (or every seen
  *   t_ij is -infinity).
- * Values of keys that a query does not see have no influence on it, infinities and NaN included.
+ * Values of keys that a query does not see have no influence on it, infinities and NaN included (with a
+ * cap: beyond the rounding of its tanh, of which there are two forms, for small and for large scores).
  * Batched (offsets NULL): sequence s is batch row s with all Lq queries; len_s = kv_lens[s] or Lk;
  *   start_s = q_starts[s] or Lk - Lq.
  * Packed documents (B = 1, q_offsets and k_offsets given, kv_lens NULL): document s has the queries
@@ -332,8 +334,8 @@ sd_status sd_rope_axes(const sd_rope_args* args, void* stream);
  *  q, o   : [B, Lq, heads, dh] views, k, v: [B, Lk, kv_heads, dh] views, bf16 (dtype 0) or fp16 (1),
  *           strides {batch, token, head} in elements, columns contiguous; 16-byte aligned, strides
  *           multiples of 8 elements (SD_ERR_MISALIGNED). Query head h reads key head
- *           h / (heads / kv_heads); kv_heads divides heads. o must not overlap q, k or v, nor fold
- *           onto itself.
+ *           h / (heads / kv_heads); kv_heads divides heads. o must not overlap q, k or v (the
+ *           views' extents are compared), nor fold onto itself.
  *  dh     : a multiple of 8 from 8 to 160.  Lq, Lk < 2^30, B * heads < 2^31. Lk = 0 gives zeros.
  *  scale  : finite and >= 0.  cap: 0 = none, else in [1e-6, 1e30], with scale / cap below 1e5.
  *  bias   : fp32 [heads, 2 * bias_radius + 1] or NULL; 0 <= bias_radius < 2^29. Values may be

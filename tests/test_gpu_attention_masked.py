@@ -203,6 +203,18 @@ def test_biases_of_minus_infinity_and_of_the_lowest_value(cuda):
             _check(o, q, k, v, bias=window)
 
 
+@pytest.mark.parametrize("R", [0, 1, 40])
+def test_lowest_bias_over_whole_tiles(cuda, R):
+    # tiles whose distances all lie beyond the table: its ends hold -infinity, the lowest value or a large one
+    q, k, v = _tensors(1, 2, 2, 300, 700, 64, torch.bfloat16, 63 + R, cuda)
+    for low in (float("-inf"), torch.finfo(torch.float32).min, float(torch.finfo(torch.bfloat16).min), -1e20, -3.0, 2.5):
+        bias = torch.zeros(2, 2 * R + 1, device=cuda)
+        bias[:, 0] = bias[:, -1] = low
+        _check(sdk.sd_attention_masked(q, k, v, bias=bias), q, k, v, bias=bias)
+        kw = dict(bias=bias, q_starts=_ints([-200], cuda), causal=False)
+        _check(sdk.sd_attention_masked(q, k, v, **kw), q, k, v, **kw)
+
+
 def test_strided_views_and_more_keys_than_heads_share(cuda):
     # q, k, v in the rows of one projection, the output in a wider buffer
     B, L, H, KV, dh = 2, 150, 4, 2, 64
@@ -258,6 +270,8 @@ def test_no_keys_and_empty(cuda):
     q = torch.ones(2, 3, 5, 64, dtype=torch.bfloat16, device=cuda)
     none = torch.ones(2, 3, 0, 64, dtype=torch.bfloat16, device=cuda)
     assert (sdk.sd_attention_masked(q, none, none) == 0).all()
+    odd = torch.ones(2, 0, 3, 61, dtype=torch.bfloat16, device=cuda).transpose(1, 2)[..., :56]  # strides that no tensor map takes
+    assert (sdk.sd_attention_masked(q[..., :56], odd, odd) == 0).all()
     assert (sdk.sd_attention_masked(q, none, none, causal=True, cap=3.0, bias=_bias(3, 4, 1, cuda)) == 0).all()
     assert sdk.sd_attention_masked(q[:, :, :0], q, q).shape == (2, 3, 0, 64)
     assert sdk.sd_attention_masked(q[:0], q[:0], q[:0]).shape == (0, 3, 5, 64)

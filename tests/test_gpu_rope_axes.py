@@ -132,6 +132,31 @@ def test_fused_projection_in_place_and_layouts(cuda, dtype):
     assert torch.equal(out[:, :, :H], qo) and torch.equal(out[:, :, H:], ko)
 
 
+def test_keys_alone_and_token_slices_of_fused_rows(cuda):
+    # heads = 0 (a call of the C interface): k alone, few tokens and many
+    axes, dh = (64,), 64
+    freqs = sdk.rope_frequencies(axes)
+    for L in (1, 9, 9000):
+        _, k, pos, _ = _inputs(1, L, 1, 3, dh, torch.bfloat16, 20 + L, cuda, axes)
+        want, _ = sdk.sd_rope_axes(k, None, pos, freqs, axes)
+        out = torch.zeros_like(k)
+        s = (L * 3 * dh, 3 * dh, dh)
+        args = sdk._ROPE_ARGS.pack(0, k.data_ptr(), 0, out.data_ptr(), 0, 0, pos.data_ptr(), freqs.data_ptr(), 1, L, 0, 3, dh, 0, 0, 0, *s, 0, 0, 0, *s,
+                                   L, 64, 0, 0, 0, 1, 0, 0, 1e-6)
+        assert sdk.lib().sd_rope_axes(args, torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(out, want)
+    # the later tokens of a fused projection's rows, in place: q and k interleave but do not meet
+    rows = torch.randn(3, 20, 7, dh, generator=torch.Generator().manual_seed(21)).to(torch.bfloat16).to(cuda)
+    q, k = rows[:, 5:, :4], rows[:, 5:, 4:6]
+    pos = torch.arange(15, dtype=torch.int32, device=cuda).view(15, 1)
+    before = rows.clone()
+    qo, ko = sdk.sd_rope_axes(q, k, pos, freqs, axes)
+    sdk.sd_rope_axes(q, k, pos, freqs, axes, q_out=q, k_out=k)
+    assert torch.equal(q, qo) and torch.equal(k, ko) and torch.equal(rows[:, :5], before[:, :5]) and torch.equal(rows[:, :, 6:], before[:, :, 6:])
+    with pytest.raises(sdk.SDError, match="overlaps"):
+        sdk.sd_rope_axes(rows[:, 5:, :4], rows[:, 5:, 3:5], pos, freqs, axes, q_out=rows[:, 5:, :4], k_out=rows[:, 5:, 3:5])
+
+
 def test_inverse_and_gradient(cuda):
     # the inverse table undoes the rotation, and the rotation's gradient is the inverse applied to it
     axes = (16, 24, 24)

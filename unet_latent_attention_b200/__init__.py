@@ -492,7 +492,7 @@ def sd_rope_axes(q, k, positions, freqs, axis_dims, pairs: str = "interleaved", 
     return q_out, k_out
 
 
-def sd_attention_masked(q, k, v, scale: float | None = None, layout: str = "bhld", causal: bool = False, cap: float = 0.0,
+def sd_attention_masked(q, k, v, scale: float | None = None, layout: str = "bhld", causal: bool = False, cap: float | None = None,
                         bias=None, kv_lens=None, q_starts=None, prefix_lens=None, q_offsets=None, k_offsets=None,
                         out=None):
     """Attention with masks, a tanh cap of the scores and a bias by distance.
@@ -553,6 +553,7 @@ def sd_attention_masked(q, k, v, scale: float | None = None, layout: str = "bhld
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have the shape and type of q")
     dev = _device_index((q, k, v, out, bias, kv_lens, q_starts, prefix_lens, q_offsets, k_offsets))
+    cap = 0.0 if cap is None else cap
     a = _ATTENTION_MASKED_ARGS.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(bias), _ptr(kv_lens), _ptr(q_starts), _ptr(prefix_lens),
         _ptr(q_offsets), _ptr(k_offsets), B, H, KV, Lq, Lk, dh, *_strides(q, blhd, "q"), *_strides(k, blhd, "k"),

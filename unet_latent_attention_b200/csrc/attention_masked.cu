@@ -111,7 +111,10 @@ extern "C" sd_status sd_attention_masked(const sd_attention_masked_args* args, v
     if (in.n[1] && sd::overlaps(o.ptr, o.bytes(), in.ptr, in.bytes()))
       return sd::fail(SD_ERR_INVALID_ARG, "sd_attention_masked: o overlaps %s", in.name);
   sd_attention_masked_args b = a;
-  if (a.Lk == 0) b.k = b.v = b.q;  // no key: nothing is loaded, but tensor maps have no empty dimension
+  if (a.Lk == 0) {  // no key: nothing is loaded, but a tensor map has no empty dimension and checks its strides
+    b.k = b.v = b.q;
+    for (int i = 0; i < 3; ++i) b.k_stride[i] = b.v_stride[i] = b.dh;
+  }
   sd::masked::Launch l{&b, a.heads / a.kv_heads, static_cast<cudaStream_t>(stream)};
   if (a.dh <= 64) return sd::masked::launch_dh64(l);
   if (a.dh <= 128) return sd::masked::launch_dh128(l);

@@ -617,6 +617,12 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         const float* w = reinterpret_cast<const float*>(smem + C::BIAS_OFF) + ((j - j0) % VS) * 4 * C::WINDOW;
         if (is_far(d0, BM + BN - 1, p.radius)) {
           offset = w[0];
+          if (!(fabsf(offset) < 1e6f)) {  // -infinity, or a type's lowest value: it swallows the score, as in a sum
+#pragma unroll
+            for (int i = 0; i < BN; i += 2) fma2(sv[i], sv[i + 1], sv[i], sv[i + 1], scale, scale, offset, offset);
+            scale = 1.f;
+            offset = 0.f;
+          }
         } else {
           // Column i of this row: value e + i, at multiples of four in the copy shifted by c.
           const int e = BM - 1 - r_in, c = 4 - (e & 3);

@@ -263,7 +263,7 @@ sd_status launch(RopeKernelArgs a, int64_t tokens, int per, cudaStream_t s) {
   a.teams = kThreads / LANES / per;
   a.all_tokens = static_cast<unsigned>(tokens);
   const int heads = a.heads + a.kv_heads;
-  a.q_teams = a.teams;
+  a.q_teams = BOTH || a.heads ? a.teams : 0;
   if (!BOTH && a.heads && a.kv_heads && a.teams > 1)  // none has much more to do than another
     a.q_teams = std::min(std::max((a.teams * a.heads + heads / 2) / heads, 1), a.teams - 1);
   a.batches = std::max(batches(a.heads, a.q_teams), batches(a.kv_heads, a.teams - a.q_teams));
@@ -326,11 +326,12 @@ struct View {
     for (int i = 0; i < 3; ++i) last += (n[i] - 1) * stride[i];
     return last * size;
   }
-  // One row per token, if the tokens of all batches are equally far apart.
+  // One row per token, if the tokens lie on one lattice (those between the batches' included).
   bool as_rows(sd::rows::RowSpan* r) const {
-    if (n[0] > 1 && stride[0] != n[1] * stride[1]) return false;
-    *r = {ptr, (n[1] > 1 ? stride[1] : stride[0]) * size, ((n[2] - 1) * stride[2] + dh) * size};
-    return n[0] * n[1] > 1 && r->stride >= r->bytes;
+    const int64_t step = n[1] > 1 ? stride[1] : stride[0];
+    if (n[0] * n[1] <= 1 || step <= 0 || (n[0] > 1 && stride[0] % step)) return false;
+    *r = {ptr, step * size, ((n[2] - 1) * stride[2] + dh) * size};
+    return r->stride >= r->bytes;
   }
   // Whether two of its heads share an element.
   bool folds() const {
@@ -350,8 +351,10 @@ struct View {
 // by their extents.
 bool meet(const View& a, const View& b) {
   sd::rows::RowSpan ra, rb;
-  if (a.as_rows(&ra) && b.as_rows(&rb) && ra.stride == rb.stride) return sd::rows::overlap(ra, rb, a.n[0] * a.n[1]);
-  return sd::overlaps(a.ptr, a.bytes(), b.ptr, b.bytes());
+  if (!sd::overlaps(a.ptr, a.bytes(), b.ptr, b.bytes())) return false;
+  if (!a.as_rows(&ra) || !b.as_rows(&rb) || ra.stride != rb.stride) return true;
+  const int64_t rows = (std::max(a.bytes(), b.bytes()) + ra.stride - 1) / ra.stride;
+  return sd::rows::overlap(ra, rb, rows);
 }
 
 sd_status check_view(const char* name, const View& v, bool output) {
