@@ -21,18 +21,18 @@
 //    running maximum is raised only when it grows by more than 2^8.
 // Two CTAs share an SM (up to 128 columns): while one waits for S, P V or a copy, the other has the
 // special-function unit, and one's start and end hide behind the other's tiles. No waiting is shared
-// between them, so items of any length mix. (Two query tiles in one CTA, with turns on the
-// special-function unit, took 192 us where this takes 150 for [2, 10, 4096, 64], and 187 where this takes 140 for [2, 8, 4096,
-// 128]; eight softmax warps on half rows 193 and 164 with one CTA, 160 with two at 64 columns.)
+// between them, so items of any length mix. Measured for [2, 10, 4096, 64] and [2, 8, 4096, 128]: 148 and 139
+// us; two query tiles in one CTA, with turns on the special-function unit, 192 and 187; eight softmax
+// warps on half rows 193 and 164 with one CTA an SM, 160 at 64 columns with two.
 //
 // Few query rows: the CTAs of a cluster take equal parts of the key tiles and join (m, l, O) through
 // distributed shared memory in rank order, so the result does not depend on timing and no workspace
 // is needed. Heads that share a key head are rows of the same tile then.
 //
-// What bounds it (B200, cycles of a softmax warp per 128 keys, two CTAs, 64 columns, no bias or cap): exp2
-// 1400 of 2800, where the special-function unit alone needs 1024 for one CTA's tile; 440 waiting for S, 560 for
-// maxima, masks and copies. Of 2 * 16 * 10 * 2 query tiles 296 run at a time, so a call of few waves
-// also waits for its last one.
+// What bounds it (cycles of a softmax warp per 128 keys, two CTAs an SM, 64 columns, no bias or cap): exp2
+// takes 1400 of 2800, where the special-function unit needs 1024 for each CTA's tile; 440 go to waiting for
+// S, the others to maxima, masks and copies. 296 query tiles run at a time, so a call of few waves also
+// waits for its last one.
 //
 // All waits on mbarriers are bounded; see attn_common.cuh.
 #pragma once
