@@ -291,30 +291,34 @@ def sd_cfg_dpmpp_3m_step(x, eps_u, eps_c, d_prev, d_prev2, w: float, alpha_prev2
     return out, d_out
 
 
-def _device_index(tensors) -> int:
-    """The index of the CUDA device that holds all ``tensors`` (None entries are skipped; views may be strided)."""
-    dev = -1
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d < 0 or not t.is_cuda:
-                raise ValueError("sd kernels run on CUDA tensors only (no CPU fallback)")
-            if d != dev:
-                if dev >= 0:
-                    raise ValueError("all tensors must be on one CUDA device")
-                dev = d
+def _device_index(first, others) -> int:
+    """The index of the CUDA device that holds all the tensors (None entries are skipped; views may be strided)."""
+    dev = first.get_device()
+    if dev < 0 or not first.is_cuda:
+        raise ValueError("sd kernels run on CUDA tensors only (no CPU fallback)")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("sd kernels run on CUDA tensors only (no CPU fallback)" if t.get_device() < 0
+                             else "all tensors must be on one CUDA device")
     return dev
+
+
+_torch_c = None
 
 
 def _call(name, dev: int, *args) -> None:
     """One library call on the current stream of device ``dev``, with ``dev`` as the current device."""
-    import torch
+    global _torch_c
+    if _torch_c is None:
+        import torch
+        _torch_c = torch._C
     f = getattr(_lib or lib(), name)
-    if torch._C._cuda_getDevice() == dev:
-        st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if _torch_c._cuda_getDevice() == dev:
+        st = f(*args, _torch_c._cuda_getCurrentRawStream(dev))
     else:
+        import torch
         with torch.cuda.device(dev):
-            st = f(*args, torch._C._cuda_getCurrentRawStream(dev))
+            st = f(*args, _torch_c._cuda_getCurrentRawStream(dev))
     if st != SD_OK:
         _check(name, st)
 
@@ -372,16 +376,24 @@ def _rms(func, x, weight, eps, residual, out, residual_out, scales, block):
         wf32 = int(weight.dtype == torch.float32)
         if weight.shape != (C,) or not (wf32 or weight.dtype == dtype) or not weight.is_contiguous():
             raise ValueError("weight must be [C], contiguous, fp32 or of the type of x")
-    dev = _device_index((x, weight, residual, out, residual_out, scales))
+    dev = _device_index(x, (weight, residual, out, residual_out, scales))
     rows = x.numel() // C if C else 0
-    xs, rs, ys, ros = (C if t is None or t.is_contiguous() else _row_stride(t, name) for t, name in
-                       ((x, "x"), (residual, "residual"), (out, "out"), (residual_out, "residual_out")))
+    xs = C if x.is_contiguous() else _row_stride(x, "x")
+    ys = C if out.is_contiguous() else _row_stride(out, "out")
+    rs = ros = C
+    rp = rop = 0
+    if residual is not None:
+        rp, rop = residual.data_ptr(), residual_out.data_ptr()
+        if not residual.is_contiguous():
+            rs = _row_stride(residual, "residual")
+        if not residual_out.is_contiguous():
+            ros = _row_stride(residual_out, "residual_out")
+    wp = 0 if weight is None else weight.data_ptr()
     if scales is None:
-        _call(func, dev, x.data_ptr(), _ptr(residual), _ptr(weight), out.data_ptr(), _ptr(residual_out), rows, C, xs, rs, ys,
-              ros, eps, code, wf32)
+        _call(func, dev, x.data_ptr(), rp, wp, out.data_ptr(), rop, rows, C, xs, rs, ys, ros, eps, code, wf32)
     else:
-        _call(func, dev, x.data_ptr(), _ptr(residual), _ptr(weight), out.data_ptr(), scales.data_ptr(), _ptr(residual_out),
-              rows, C, xs, rs, ys, ros, eps, code, wf32, block)
+        _call(func, dev, x.data_ptr(), rp, wp, out.data_ptr(), scales.data_ptr(), rop, rows, C, xs, rs, ys, ros, eps, code,
+              wf32, block)
     return residual_out
 
 
@@ -429,10 +441,10 @@ def sd_rms_norm_fp8(x, weight=None, eps: float = 1e-6, residual=None, block: int
 
 def _strides(t, blhd, name):
     """{batch, token, head} strides of a 4-D view with contiguous columns."""
-    s = t.stride()
-    if s[3] != 1 and t.shape[3] > 1:
+    b, m, n, c = t.stride()
+    if c != 1 and t.shape[3] > 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return (s[0], s[1], s[2]) if blhd else (s[0], s[2], s[1])
+    return (b, m, n) if blhd else (b, n, m)
 
 
 def sd_rope_axes(q, k, positions, freqs, axis_dims, pairs: str = "interleaved", layout: str = "blhd", q_weight=None,
@@ -453,15 +465,22 @@ def sd_rope_axes(q, k, positions, freqs, axis_dims, pairs: str = "interleaved", 
     blhd = layout == "blhd"
     if q.dim() != 4:
         raise ValueError("q must be 4-D")
-    B, L, H = (q.shape[0], q.shape[1], q.shape[2]) if blhd else (q.shape[0], q.shape[2], q.shape[1])
-    dh = q.shape[3]
+    if blhd:
+        B, L, H, dh = q.shape
+    else:
+        B, H, L, dh = q.shape
     axes = len(axis_dims)
     if not 1 <= axes <= 4:
         raise ValueError("1 to 4 axes")
-    if k is not None and (k.dim() != 4 or k.dtype != q.dtype or k.shape[0] != B or k.shape[1 if blhd else 2] != L
-                          or k.shape[3] != dh):
-        raise ValueError("k must match q in type, batch, length and head dim")
-    if positions.dtype != torch.int32 or tuple(positions.shape) not in ((B, L, axes), (L, axes)) or not positions.is_contiguous():
+    KV = 0
+    if k is not None:
+        if k.dim() != 4 or k.dtype != q.dtype:
+            raise ValueError("k must match q in type, batch, length and head dim")
+        Bk, m, n, dhk = k.shape
+        Lk, KV = (m, n) if blhd else (n, m)
+        if Bk != B or Lk != L or dhk != dh:
+            raise ValueError("k must match q in type, batch, length and head dim")
+    if positions.dtype != torch.int32 or positions.shape not in ((B, L, axes), (L, axes)) or not positions.is_contiguous():
         raise ValueError("positions must be contiguous int32 [B, L, axes] or [L, axes]")
     if freqs.dtype != torch.int64 or freqs.shape != (sum(axis_dims) // 2,) or not freqs.is_contiguous():
         raise ValueError("freqs must be int64 [sum(axis_dims) / 2]")
@@ -479,17 +498,23 @@ def sd_rope_axes(q, k, positions, freqs, axis_dims, pairs: str = "interleaved", 
         k_out = torch.empty_like(k)
     elif k_out.shape != k.shape or k_out.dtype != k.dtype:
         raise ValueError("k_out must have the shape and type of k")
-    dev = _device_index((q, k, positions, freqs, q_weight, k_weight, q_out, k_out))
+    dev = _device_index(q, (k, positions, freqs, q_weight, k_weight, q_out, k_out))
     k_there = k is not None
     dims = tuple(axis_dims)
     a = _ROPE_ARGS.pack(
         q.data_ptr(), k.data_ptr() if k_there else 0, q_out.data_ptr(), k_out.data_ptr() if k_there else 0, _ptr(q_weight),
-        _ptr(k_weight), positions.data_ptr(), freqs.data_ptr(), B, L, H, k.shape[2 if blhd else 1] if k_there else 0, dh,
+        _ptr(k_weight), positions.data_ptr(), freqs.data_ptr(), B, L, H, KV, dh,
         *_strides(q, blhd, "q"), *(_strides(k, blhd, "k") if k_there else (0, 0, 0)), *_strides(q_out, blhd, "q_out"),
         *(_strides(k_out, blhd, "k_out") if k_there else (0, 0, 0)), L * axes if positions.dim() == 3 else 0,
         *dims, *(0, 0, 0)[axes - 1:], axes, pairs == "half", code, eps)
     _call("sd_rope_axes", dev, a)
     return q_out, k_out
+
+
+def _check_ints(name, t, n) -> None:
+    import torch
+    if t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 [{n}]")
 
 
 def sd_attention_masked(q, k, v, scale: float | None = None, layout: str = "bhld", causal: bool = False, cap: float | None = None,
@@ -519,10 +544,11 @@ def sd_attention_masked(q, k, v, scale: float | None = None, layout: str = "bhld
     if layout not in ("bhld", "blhd"):
         raise ValueError("layout must be 'bhld' or 'blhd'")
     blhd = layout == "blhd"
-    B, dh = q.shape[0], q.shape[3]
-    Lq, H = (q.shape[1], q.shape[2]) if blhd else (q.shape[2], q.shape[1])
-    Lk, KV = (k.shape[1], k.shape[2]) if blhd else (k.shape[2], k.shape[1])
-    if k.shape[0] != B or k.shape[3] != dh or v.shape != k.shape:
+    if blhd:
+        (B, Lq, H, dh), (Bk, Lk, KV, dhk) = q.shape, k.shape
+    else:
+        (B, H, Lq, dh), (Bk, KV, Lk, dhk) = q.shape, k.shape
+    if Bk != B or dhk != dh or v.shape != k.shape:
         raise ValueError("k and v must match each other, and q in batch and head dim")
     if (q_offsets is None) != (k_offsets is None):
         raise ValueError("q_offsets and k_offsets go together")
@@ -535,11 +561,14 @@ def sd_attention_masked(q, k, v, scale: float | None = None, layout: str = "bhld
         docs = q_offsets.numel() - 1
         if docs < 1 or k_offsets.numel() != docs + 1:
             raise ValueError("q_offsets and k_offsets must both be [docs + 1], docs >= 1")
-    n_seq = docs or B
-    for name, t, n in (("kv_lens", kv_lens, n_seq), ("q_starts", q_starts, n_seq), ("prefix_lens", prefix_lens, n_seq),
-                       ("q_offsets", q_offsets, docs + 1), ("k_offsets", k_offsets, docs + 1)):
-        if t is not None and (t.dtype != torch.int32 or t.shape != (n,) or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous int32 [{n}]")
+        _check_ints("q_offsets", q_offsets, docs + 1)
+        _check_ints("k_offsets", k_offsets, docs + 1)
+    if kv_lens is not None:
+        _check_ints("kv_lens", kv_lens, B)
+    if q_starts is not None:
+        _check_ints("q_starts", q_starts, docs or B)
+    if prefix_lens is not None:
+        _check_ints("prefix_lens", prefix_lens, docs or B)
     if prefix_lens is not None and not causal:
         raise ValueError("prefix_lens needs causal")
     radius = 0
@@ -552,7 +581,7 @@ def sd_attention_masked(q, k, v, scale: float | None = None, layout: str = "bhld
         out = torch.zeros_like(q) if docs else torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have the shape and type of q")
-    dev = _device_index((q, k, v, out, bias, kv_lens, q_starts, prefix_lens, q_offsets, k_offsets))
+    dev = _device_index(q, (k, v, out, bias, kv_lens, q_starts, prefix_lens, q_offsets, k_offsets))
     cap = 0.0 if cap is None else cap
     a = _ATTENTION_MASKED_ARGS.pack(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), _ptr(bias), _ptr(kv_lens), _ptr(q_starts), _ptr(prefix_lens),
