@@ -661,7 +661,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       const float mx = max3f(max3f(pm[0], pm[1], pm[2]), max3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
       // A row without a seen key keeps m = -infinity whatever the offset is.
       const float m_new = fmaxf(m_run, C::BIAS ? (mx == -INFINITY ? mx : fmaf(mx, scale, offset)) : mx * scale);
-      // Row by row: no row's bits depend on its neighbours' scores.
+      // Row by row: a row's maximum never depends on its neighbours' scores.
       const bool raise = m_new > m_run + 8.0f, rescale = __any_sync(0xffffffffu, raise);
       const float alpha = !raise ? 1.0f : m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
       if (raise) m_run = m_new;

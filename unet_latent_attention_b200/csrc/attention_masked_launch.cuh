@@ -97,12 +97,13 @@ sd_status choose(const Launch& l) {
   return launch<C>(l, pack, tiles, splits);
 }
 
-template <int DHT, int BN, int KS, int VS, int CTAS, bool F16>
+// KS, VS: stages of K and V; BKS, BVS: beside a bias's windows.
+template <int DHT, int BN, int KS, int VS, int CTAS, bool F16, int BKS = KS, int BVS = VS>
 sd_status by_score(const Launch& l) {
   const bool cap = l.args->cap != 0.f, bias = l.args->bias != nullptr;
-  if (cap && bias) return choose<Cfg<DHT, BN, KS, VS, CTAS, F16, true, true>>(l);
+  if (cap && bias) return choose<Cfg<DHT, BN, BKS, BVS, CTAS, F16, true, true>>(l);
   if (cap) return choose<Cfg<DHT, BN, KS, VS, CTAS, F16, true, false>>(l);
-  if (bias) return choose<Cfg<DHT, BN, KS, VS, CTAS, F16, false, true>>(l);
+  if (bias) return choose<Cfg<DHT, BN, BKS, BVS, CTAS, F16, false, true>>(l);
   return choose<Cfg<DHT, BN, KS, VS, CTAS, F16, false, false>>(l);
 }
 
