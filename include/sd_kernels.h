@@ -333,7 +333,8 @@ sd_status sd_rope_axes(const sd_rope_args* args, void* stream);
  *   are left as they were.
  *  q, o   : [B, Lq, heads, dh] views, k, v: [B, Lk, kv_heads, dh] views, bf16 (dtype 0) or fp16 (1),
  *           strides {batch, token, head} in elements, columns contiguous; 16-byte aligned, strides
- *           multiples of 8 elements (SD_ERR_MISALIGNED). Query head h reads key head
+ *           multiples of 8 elements (SD_ERR_MISALIGNED), at least dh and below 2^38 where there is more
+ *           than one element to step over (SD_ERR_UNSUPPORTED: no broadcast views). Query head h reads key head
  *           h / (heads / kv_heads); kv_heads divides heads. o must not overlap q, k or v (the
  *           views' extents are compared), nor fold onto itself.
  *  dh     : a multiple of 8 from 8 to 160.  Lq, Lk < 2^30, B * heads < 2^31. Lk = 0 gives zeros.
