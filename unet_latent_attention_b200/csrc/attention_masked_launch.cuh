@@ -90,7 +90,8 @@ sd_status choose(const Launch& l) {
   const int64_t planes = a.B * (a.heads / pack), tiles = (a.Lq * pack + BM - 1) / BM;
   // Idle SMs: split the keys over a cluster, two key tiles a CTA at least, while all clusters run at once.
   // (Beyond that the clusters' starts, joins and ends cost more than they even out: B200, [32, 16, 1, 2048
-  // ragged, 64] takes 52, 61, 91 and 167 us with 1, 2, 4 and 8 parts; [4, 32 / 8 heads, 1, 16384, 128] 232, 122, 68 and 49.)
+  // ragged, 64] takes 52, 61, 91 and 167 us with 1, 2, 4 and 8 parts; [4, 32 / 8 heads, 1, 16384, 128] 232, 122, 68 and 49;
+  // [16, 16 / 4 heads, 1, 8192 ragged, 128] 39 with 4 parts and 46 with 8.)
   int splits = 1;
   const int64_t key_tiles = (a.Lk + C::BN - 1) / C::BN;
   while (2 * splits <= kMaxSplits && planes * tiles * 2 * splits <= C::CTAS * sd::sm_count() && key_tiles >= 4 * splits) splits *= 2;
