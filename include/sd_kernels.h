@@ -338,6 +338,8 @@ sd_status sd_rope_axes(const sd_rope_args* args, void* stream);
  *           h / (heads / kv_heads); kv_heads divides heads. o must not overlap q, k or v (the
  *           views' extents are compared), nor fold onto itself.
  *  dh     : a multiple of 8 from 8 to 160.  Lq, Lk < 2^30, B * heads < 2^31. Lk = 0 gives zeros.
+ * The sums q.k have to stay within fp32, with a bias and no cap also the scores (times log2(e)); within that
+ *   scores may be of any size.
  *  scale  : finite and >= 0.  cap: 0 = none, else in [1e-6, 1e30], with scale / cap below 1e5.
  *  bias   : fp32 [heads, 2 * bias_radius + 1] or NULL; 0 <= bias_radius < 2^29. Values may be
  *           -infinity, or the lowest of a type; +infinity and NaN spread over their rows.

@@ -1,0 +1,108 @@
+"""GPU parity of sd_attention_masked where scores are large, infinite or at the ends of their type.
+
+Products q.k are small integers (or 2^20 and small integers), so the tensor cores' fp32 sums hold them exactly
+and both sides have the same ties. What is left of a weight's error: ex2.approx (2^-22 relative), the
+difference from the maximum and its product with the scale (2^-23 |x| at a weight of 2^-x: below 1e-7), the
+rounded product of a maximum of up to 2^16 (half a step, 2^-8 * ln 2, for the keys before a raise of the
+maximum, whose weights are below 2^-8 by then: 1.1e-5) and sums of at most 64 dependent terms (64 * 2^-24 =
+4e-6). ARITH = 5e-5 is above them together, for the numerator and for the denominator; the weights are rounded
+to the inputs' type (half a step u), fp16 weights below 2^-14 to 2^-25, and the output once more."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import unet_latent_attention_b200 as sdk
+
+pytestmark = pytest.mark.gpu
+
+ARITH = 5e-5
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+def _ints(v, dev):
+    return torch.tensor(v, dtype=torch.int32, device=dev)
+
+
+def _whole_numbers(B, H, KV, Lq, Lk, dh, t, seed, dev):
+    """q and k of whole numbers from -3 to 3 (|q.k| <= 9 dh), normal v."""
+    g = torch.Generator().manual_seed(seed)
+    q, k = (torch.randint(-3, 4, s, generator=g).float() for s in ((B, H, Lq, dh), (B, KV, Lk, dh)))
+    v = torch.randn(B, KV, Lk, dh, generator=g)
+    return tuple(x.to(t).to(dev) for x in (q, k, v))
+
+
+def _check(o, q, k, v, **kw):
+    sdk.sd_device_status()
+    host = {n: (x.cpu().numpy() if torch.is_tensor(x) and x.dtype == torch.int32 else x) for n, x in kw.items()}
+    ref, a = oracle.attention_masked(q, k, v, **host)
+    got = o.double().cpu().numpy()
+    u = torch.finfo(q.dtype).eps / 2
+    tiny = 2.0 ** -25 * np.abs(v.double().cpu().numpy()).sum(axis=2).max() if q.dtype == torch.float16 else 0.0
+    assert np.isfinite(got).all()
+    tol = (u + 2 * ARITH) * a * (1 + u) + u * np.abs(ref) + tiny + 1e-30
+    assert (np.abs(got - ref) <= tol).all(), float((np.abs(got - ref) - tol).max())
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("scale", [100.0, 1e5, 1e9, 1e30, 3e38])
+@pytest.mark.parametrize("dh", [64, 128, 160])
+def test_large_scales(cuda, dh, scale, dtype):
+    # a row's largest score has the weight 1 (shared by its ties), however large the score is
+    B, H, KV, Lq, Lk = 2, 4, 2, 200, 333
+    q, k, v = _whole_numbers(B, H, KV, Lq, Lk, dh, TYPES[dtype], dh, cuda)
+    lens, prefix = _ints([333, 150], cuda), _ints([0, 77], cuda)
+    for kw in (dict(), dict(causal=True), dict(kv_lens=lens), dict(causal=True, kv_lens=lens, prefix_lens=prefix)):
+        kw = dict(kw, scale=scale)
+        _check(sdk.sd_attention_masked(q, k, v, **kw), q, k, v, **kw)
+    if scale < 1e37:  # with a bias the score itself has to stay in fp32
+        for R in (0, 5):  # one value a head: it moves no tie; tiles beyond the table and across it
+            bias = torch.tensor([0.5, -2.0, 7.0, 0.0], device=cuda)[:, None].expand(H, 2 * R + 1).contiguous()
+            kw = dict(bias=bias, causal=True, scale=scale)
+            _check(sdk.sd_attention_masked(q, k, v, **kw), q, k, v, **kw)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("scale", [1e9, 3e38])
+def test_large_scales_of_few_queries_and_documents(cuda, scale, dtype):
+    # keys split over a cluster, whose parts have maxima of their own
+    q, k, v = _whole_numbers(2, 4, 2, 1, 4000, 128, TYPES[dtype], 5, cuda)
+    for kw in (dict(), dict(kv_lens=_ints([4000, 900], cuda))):
+        kw = dict(kw, scale=scale)
+        _check(sdk.sd_attention_masked(q, k, v, **kw), q, k, v, **kw)
+    q, k, v = _whole_numbers(1, 2, 2, 300, 300, 64, TYPES[dtype], 6, cuda)
+    off = _ints([0, 70, 71, 290], cuda)
+    kw = dict(q_offsets=off, k_offsets=off, scale=scale)
+    _check(sdk.sd_attention_masked(q, k, v, **kw), q, k, v, **kw)
+    if scale < 1e37:
+        kw.update(k_offsets=_ints([0, 100, 120, 300], cuda), bias=torch.full((2, 9), 3.0, device=cuda))  # different shifts in one tile
+        _check(sdk.sd_attention_masked(q, k, v, **kw), q, k, v, **kw)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("Lq,Lk", [(200, 333), (1, 3000)])
+def test_scores_around_a_large_value(cuda, Lq, Lk, sign, dtype):
+    # q.k = +-2^20 + a small whole number: an ordinary softmax around +-2^17, and a flat one around +-2^13
+    q, k, v = _whole_numbers(1, 2, 2, Lq, Lk, 64, TYPES[dtype], 7, cuda)
+    q[..., 0], k[..., 0] = 1024.0, sign * 1024.0
+    for kw in (dict(scale=0.125), dict(scale=0.125, causal=True), dict(scale=0.0078125, causal=True)):
+        _check(sdk.sd_attention_masked(q, k, v, **kw), q, k, v, **kw)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_a_large_score_in_one_row(cuda, dtype):
+    # its neighbours keep their bits, and a tile of large scores after one of small ones takes over
+    q, k, v = _whole_numbers(1, 2, 2, 150, 400, 64, TYPES[dtype], 8, cuda)
+    want = sdk.sd_attention_masked(q, k, v, scale=0.125)
+    q2 = q.clone()
+    q2[:, :, 40] = 2.0 ** 14 * q[:, :, 40]
+    o = sdk.sd_attention_masked(q2, k, v, scale=1e3)
+    _check(o, q2, k, v, scale=1e3)
+    o = sdk.sd_attention_masked(q2, k, v, scale=0.125)
+    rest = [i for i in range(150) if i != 40]
+    assert torch.equal(o[:, :, rest], want[:, :, rest])
+    _check(o, q2, k, v, scale=0.125)
+    k2 = k.clone()
+    k2[:, :, 256:] = 2.0 ** 13 * k[:, :, 256:]
+    _check(sdk.sd_attention_masked(q, k2, v, scale=1e4), q, k2, v, scale=1e4)

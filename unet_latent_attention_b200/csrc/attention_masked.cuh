@@ -148,6 +148,11 @@ struct Cfg {
   static constexpr int TM_P = BN, TM_O = BN + BN / 2;  // tensor memory columns: S | P | O
   static constexpr int TM_COLS = TM_O + DHT <= 256 ? 256 : 512;
   static constexpr int THREADS = 256;
+  // Units of a row's maximum: those of q.k where nothing else makes up a score, else those of the score (log2).
+  static constexpr bool RAW_MAX = !CAP && !BIAS;
+  // Rows whose maximum passes this (units of log2) take exp2's argument from differences; see the softmax.
+  static constexpr float LARGE = 65536.f;
+  static constexpr bool CHECK_LARGE = !CAP;  // a cap's scores are differences from the start
   static constexpr int REG_HELPER = 48, REG_SOFT = 208;  // two CTAs an SM: registers move to the softmax warps
   // Join of a cluster's parts: rows of DHT fp32 and (m, l), over Q and the rings.
   static constexpr int JOIN_ROW = DHT + 4;  // floats a row (+4: rows start in different banks)
@@ -543,6 +548,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
     const bool is_mixed = C::BIAS && *mixed;
     const int ochunks = (p.dh + 15) / 16;
     float m_run = -INFINITY, l_run = 0.f;
+    const float m_scale = C::RAW_MAX ? p.scale_log2 : 1.f;
     bool ok = true;
     if (!live) {
       for (int j = j0; ok && j < j1; ++j) {
@@ -610,14 +616,17 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           if (is_mixed) scale = 1.f;
         }
       }
-      tc_fence_before();
-      mbar_arrive(bars.s_free());
+      if constexpr (!C::CHECK_LARGE) {
+        tc_fence_before();
+        mbar_arrive(bars.s_free());
+      }
       if (C::BIAS && !biased) {
         const long long d0 = static_cast<long long>(j) * BN - (q_first + BM - 1) + shift0;  // the window's first distance
         const float* w = reinterpret_cast<const float*>(smem + C::BIAS_OFF) + ((j - j0) % VS) * 4 * C::WINDOW;
         if (is_far(d0, BM + BN - 1, p.radius)) {
-          offset = w[0];
-          if (!(fabsf(offset) < 1e6f)) {  // -infinity, or a type's lowest value: it swallows the score, as in a sum
+          offset = w[0] == 0.f ? -0.f : w[0];  // +0 says that the sums are formed already
+          // -infinity, or a type's lowest value: it swallows the score, as in a sum. (So does a large cap's score.)
+          if (!(fabsf(offset) < 1e6f) || (C::CAP && p.cap_out > C::LARGE)) {
 #pragma unroll
             for (int i = 0; i < BN; i += 2) fma2(sv[i], sv[i + 1], sv[i], sv[i + 1], scale, scale, offset, offset);
             scale = 1.f;
@@ -660,13 +669,21 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       for (int k = 0; k < 8; ++k) pm[k] = fmaxf(pm[k], sv[BN - 8 + k]);
       const float mx = max3f(max3f(pm[0], pm[1], pm[2]), max3f(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
       // A row without a seen key keeps m = -infinity whatever the offset is.
-      const float m_new = fmaxf(m_run, C::BIAS ? (mx == -INFINITY ? mx : fmaf(mx, scale, offset)) : mx * scale);
-      // Row by row: a row's maximum never depends on its neighbours' scores.
-      const bool raise = m_new > m_run + 8.0f, rescale = __any_sync(0xffffffffu, raise);
-      const float alpha = !raise ? 1.0f : m_run == -INFINITY ? 0.f : ex2_approx(m_run - m_new);
+      const float m_new = fmaxf(m_run, C::BIAS ? (mx == -INFINITY ? mx : fmaf(mx, scale, offset)) : mx);
+      // Row by row: a row's maximum never depends on its neighbours' scores. (-infinity - -infinity: no raise)
+      const bool raise = (m_new - m_run) * m_scale > 8.0f, rescale = __any_sync(0xffffffffu, raise);
+      const float alpha = !raise ? 1.0f : m_run == -INFINITY ? 0.f : ex2_approx((m_run - m_new) * m_scale);
       if (raise) m_run = m_new;
       // exp2(scale sv + offset - m); a row that has seen nothing gets zeros
-      const float minus_m = (m_run == -INFINITY ? 0.f : -m_run) + (C::BIAS ? offset : 0.f);
+      const float minus_m = (m_run == -INFINITY ? 0.f : -m_run * m_scale) + (C::BIAS ? offset : 0.f);
+      // minus_m is off by half a step of the row's maximum. All weights of the row share that, but a step of a
+      // large maximum is more than exp2 can hold: there the row's weights are formed again below, and S stays.
+      bool large = false;
+      if constexpr (C::CHECK_LARGE) {
+        large = (C::RAW_MAX || __float_as_uint(offset) != 0) && fabsf(m_run * m_scale) > C::LARGE && fabsf(m_run) < INFINITY;
+        tc_fence_before();
+        mbar_arrive_if(bars.s_free(), !large);
+      }
       uint32_t pk[BN / 2];
       float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
 #pragma unroll
@@ -680,6 +697,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         else add2(ls0, ls1, ls0, ls1, x0, x1);
         pk[i] = C::F16 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
       }
+      const float l_before = l_run * alpha;
       l_run = fmaf(l_run, alpha, (ls0 + ls1) + (ls2 + ls3));
       if (j > j0) {
         if (!__all_sync(0xffffffffu, wait_bar(bars.o_done(), (j - j0 - 1) & 1, abort_flag, p.err))) {
@@ -706,6 +724,41 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         tmem_st16(tP + c * 16, r);
       }
       tmem_wait_st();
+      if constexpr (C::CHECK_LARGE) {
+        // The rows of large maxima once more, from S in tensor memory: the difference from the maximum comes
+        // first and is 0 for the largest score (of q.k, or of the sum with a bias as rounded to fp32). The check
+        // costs 1 to 3% of short key tiles' time ([2, 8, 4096, 128]: 139 -> 141 us, one token of [16, 16 / 4, 8192
+        // ragged, 128] 39.0 -> 40.0) and nothing of the long ones' ([2, 10, 4096, 64]: 146); done before exp2,
+        // where it waits for the maximum, 2 to 7%.
+        if (__any_sync(0xffffffffu, large)) {
+          const int lo = me.lo - j * BN, hi = me.hi - j * BN;
+          float sum = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < BN / 32; ++c) {
+            uint32_t r[32], w[16];
+            tmem_ld32(tS + c * 32, r);
+            tmem_ld16(tP + c * 16, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float y[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float x = __uint_as_float(r[i + e]);
+                const int col = c * 32 + i + e;
+                y[e] = col < lo || col >= hi ? 0.f : ex2_approx(C::RAW_MAX ? (x - m_run) * scale : fmaf(x, scale, offset) - m_run);
+              }
+              if (large) w[i / 2] = C::F16 ? pack_f16x2(y[0], y[1]) : pack_bf16x2(y[0], y[1]);
+              sum += y[0] + y[1];
+            }
+            tmem_st16(tP + c * 16, w);
+          }
+          tmem_wait_st();
+          if (large) l_run = l_before + sum;
+          tc_fence_before();
+          if (large) mbar_arrive(bars.s_free());
+        }
+      }
       tc_fence_before();
       mbar_arrive(bars.p_full());
     }
@@ -792,11 +845,13 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         if (!row_of(p, b, static_cast<int>(at >> p.pack_log2)).exists) continue;
         float m = -INFINITY;
         for (int k = 0; k < splits; ++k) m = fmaxf(m, peer_load4(sbase + (r * C::JOIN_ROW + C::DHT) * 4, k).x);
+        const float m_scale = C::RAW_MAX ? p.scale_log2 : 1.f;
+        const bool large = fabsf(m * m_scale) > C::LARGE;  // else the parts' own shifts are these products
         float l = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         for (int k = 0; k < splits; ++k) {
           const float4 ml = peer_load4(sbase + (r * C::JOIN_ROW + C::DHT) * 4, k);
           if (ml.y == 0.f) continue;  // this part has no key that the row sees
-          const float a = ml.x == -INFINITY ? 1.f : ex2_approx(ml.x - m);
+          const float a = ml.x == -INFINITY ? 1.f : ex2_approx(large ? (ml.x - m) * m_scale : __fmul_rn(ml.x, m_scale) - __fmul_rn(m, m_scale));
           const float4 x = peer_load4(sbase + (r * C::JOIN_ROW + c) * 4, k);
           const float4 y = peer_load4(sbase + (r * C::JOIN_ROW + c + 4) * 4, k);
           l = fmaf(ml.y, a, l);

@@ -43,7 +43,8 @@ sd_status launch(const Launch& l, int pack, int64_t tiles, int splits) {
                       ? static_cast<int>(std::min<int64_t>(std::max<int64_t>((int64_t(48) << 20) / plane_bytes, 1), p.planes))
                       : 1;
   constexpr float kLog2e = 1.4426950408889634f;
-  p.scale_log2 = std::max(a.scale * kLog2e, 1.17549435e-38f);  // scale 0: a masked score must not become 0 * -infinity
+  // scale 0: a masked score must not become 0 * -infinity; a scale near fp32's end: 0 must not become 0 * infinity
+  p.scale_log2 = std::min(std::max(a.scale * kLog2e, 1.17549435e-38f), 3.402823466e38f);
   p.cap_in = C::CAP ? a.scale / a.cap : 0.f;
   p.cap_out = a.cap * kLog2e;
   p.err = sd::device_status_word();
