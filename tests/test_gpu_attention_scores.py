@@ -6,7 +6,9 @@ difference from the maximum and its product with the scale (2^-23 |x| at a weigh
 rounded product of a maximum of up to 2^16 (half a step, 2^-8 * ln 2, for the keys before a raise of the
 maximum, whose weights are below 2^-8 by then: 1.1e-5) and sums of at most 64 dependent terms (64 * 2^-24 =
 4e-6). ARITH = 5e-5 is above them together, for the numerator and for the denominator; the weights are rounded
-to the inputs' type (half a step u), fp16 weights below 2^-14 to 2^-25, and the output once more."""
+to the inputs' type (half a step u), fp16 weights below 2^-14 to 2^-25, and the output once more. A cap's tanh is
+off by 2e-7 of the score, or of the cap where the score is above half of it: below 2e-5 at a cap of 30 or at
+scores of up to 60 and larger caps."""
 import numpy as np
 import pytest
 import torch
@@ -106,3 +108,33 @@ def test_a_large_score_in_one_row(cuda, dtype):
     k2 = k.clone()
     k2[:, :, 256:] = 2.0 ** 13 * k[:, :, 256:]
     _check(sdk.sd_attention_masked(q, k2, v, scale=1e4), q, k2, v, scale=1e4)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("cap", [30.0, 1e4, 1e6])
+@pytest.mark.parametrize("dh", [64, 128])
+def test_capped_scores_do_not_depend_on_other_scores(cuda, dh, cap, dtype):
+    # beside a score above half the cap, of an unseen key or of another row, all others keep their bits
+    t = TYPES[dtype]
+    q, k, v = _whole_numbers(2, 2, 2, 150, 400, dh, t, 9 + dh, cuda)
+    for kw in (dict(kv_lens=_ints([390, 140], cuda)), dict(kv_lens=_ints([390, 140], cuda), bias=torch.randn(2, 9, generator=torch.Generator().manual_seed(1)).to(cuda))):
+        kw = dict(kw, cap=cap)
+        want = sdk.sd_attention_masked(q, k, v, **kw)
+        _check(want, q, k, v, **kw)
+        for x in (float("nan"), float("inf"), float("-inf"), torch.finfo(t).max):
+            k2 = k.clone()
+            k2[0, :, 390:], k2[1, :, 140:] = x, x
+            assert torch.equal(sdk.sd_attention_masked(q, k2, v, **kw), want), x
+        q2 = q.clone()
+        q2[:, :, 40] = torch.where(q[:, :, 40] < 0, -60000.0, 60000.0)
+        rest = [i for i in range(150) if i != 40]
+        assert torch.equal(sdk.sd_attention_masked(q2, k, v, **kw)[:, :, rest], want[:, :, rest])
+    want = sdk.sd_attention_masked(q, k, v, causal=True, cap=cap)
+    k2 = k.clone()
+    k2[:, :, 300] = torch.finfo(t).max  # the last 50 rows see it
+    assert torch.equal(sdk.sd_attention_masked(q, k2, v, causal=True, cap=cap)[:, :, :50], want[:, :, :50])
+    q, k, v = _whole_numbers(2, 2, 2, 1, 3000, dh, t, 10 + dh, cuda)  # keys split over a cluster
+    kw = dict(cap=cap, kv_lens=_ints([2990, 700], cuda))
+    want = sdk.sd_attention_masked(q, k, v, **kw)
+    k[0, :, 2990:], k[1, :, 700:] = float("nan"), torch.finfo(t).max
+    assert torch.equal(sdk.sd_attention_masked(q, k, v, **kw), want)

@@ -238,16 +238,34 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// cap * log2(e) * tanh(x k) of one score, from two results of the special-function unit.
-__device__ __forceinline__ float cap_score(float x, float k, float cap_log2) {
+// cap * log2(e) * tanh(x k) of one score, from two results of the special-function unit: off by 2e-7 of the
+// cap, which only a score of its size can bear.
+__device__ __forceinline__ float cap_large_score(float x, float k, float cap_log2) {
   return fmaf(-2.f * cap_log2, rcp_approx(1.f + ex2_approx(x * (k * 2.885390081777927f))), cap_log2);
 }
 
-// The same of N scores by an odd polynomial in u = x k, for |u| <= 1/2 (scores stay below their cap by
-// design): off by 2e-7 of the cap (coefficients from unet_latent_attention_b200/fit_tanh_poly.py), in 5
-// packed operations for two values on the FMA pipe; the softmax needs the special-function unit for itself
-// ([2, 10, 4096, 64]: 226 us; 332 us with cap_score alone). False, with nothing done, if a score of the
-// warp lies beyond.
+// The same for |x k| <= 1/2 by an odd polynomial in x (coefficients from
+// unet_latent_attention_b200/fit_tanh_poly.py): off by 2e-7 of the score.
+struct CapPoly {
+  float2 c0, c1, c2, c3;  // twice each, for packed operations
+};
+__device__ __forceinline__ CapPoly cap_poly(float k, float cap_log2) {
+  const float k2 = k * k, a0 = cap_log2 * k, a1 = a0 * k2, a2 = a1 * k2, a3 = a2 * k2;
+  const float2 c0 = {9.999976754e-01f * a0, 9.999976754e-01f * a0}, c1 = {-3.332065642e-01f * a1, -3.332065642e-01f * a1}, c2 = {1.314514577e-01f * a2, 1.314514577e-01f * a2}, c3 = {-4.337248206e-02f * a3, -4.337248206e-02f * a3};
+  return {c0, c1, c2, c3};
+}
+
+// One score by its own form, so that it does not depend on its neighbours' or on those of unseen keys.
+__device__ __forceinline__ float cap_score(float x, float k, float cap_log2) {
+  const CapPoly c = cap_poly(k, cap_log2);
+  const float z = __fmul_rn(x, x), p = __fmul_rn(__fmaf_rn(__fmaf_rn(__fmaf_rn(c.c3.x, z, c.c2.x), z, c.c1.x), z, c.c0.x), x);
+  return fabsf(x) * k > 0.5f ? cap_large_score(x, k, cap_log2) : p;
+}
+
+// N scores, if all of the warp's are small (they stay below their cap by design), with the results of
+// cap_score: 5 packed operations for two values on the FMA pipe; the softmax needs the special-function unit
+// for itself ([2, 10, 4096, 64]: 223 us; 332 us with cap_large_score alone). False, with nothing done, if a score
+// of the warp lies beyond.
 template <int N>
 __device__ __forceinline__ bool cap_small_scores(float (&x)[N], float k, float cap_log2) {
   float top[4] = {0.f, 0.f, 0.f, 0.f};
@@ -256,14 +274,13 @@ __device__ __forceinline__ bool cap_small_scores(float (&x)[N], float k, float c
 #pragma unroll
     for (int e = 0; e < 4; ++e) top[e] = max3f(top[e], fabsf(x[i + e]), fabsf(x[i + 4 + e]));
   if (__any_sync(0xffffffffu, fmaxf(max3f(top[0], top[1], top[2]), top[3]) * k > 0.5f)) return false;
-  const float k2 = k * k, a0 = cap_log2 * k, a1 = a0 * k2, a2 = a1 * k2, a3 = a2 * k2;
-  const float2 c0 = {9.999976754e-01f * a0, 9.999976754e-01f * a0}, c1 = {-3.332065642e-01f * a1, -3.332065642e-01f * a1}, c2 = {1.314514577e-01f * a2, 1.314514577e-01f * a2}, c3 = {-4.337248206e-02f * a3, -4.337248206e-02f * a3};
+  const CapPoly c = cap_poly(k, cap_log2);
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     const float2 v = make_float2(x[i], x[i + 1]), z = __fmul2_rn(v, v);
-    float2 p = __ffma2_rn(c3, z, c2);
-    p = __ffma2_rn(p, z, c1);
-    p = __ffma2_rn(p, z, c0);
+    float2 p = __ffma2_rn(c.c3, z, c.c2);
+    p = __ffma2_rn(p, z, c.c1);
+    p = __ffma2_rn(p, z, c.c0);
     p = __fmul2_rn(p, v);
     x[i] = p.x, x[i + 1] = p.y;
   }
