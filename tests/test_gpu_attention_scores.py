@@ -138,3 +138,31 @@ def test_capped_scores_do_not_depend_on_other_scores(cuda, dh, cap, dtype):
     want = sdk.sd_attention_masked(q, k, v, **kw)
     k[0, :, 2990:], k[1, :, 700:] = float("nan"), torch.finfo(t).max
     assert torch.equal(sdk.sd_attention_masked(q, k, v, **kw), want)
+
+
+def test_a_large_cap_of_large_scores(cuda):
+    # q.k = 2^66 * a whole number (its square is beyond fp32) under a cap of 1e30: as if there were no cap
+    for Lq, Lk in ((150, 333), (1, 3000)):
+        q, k, v = _whole_numbers(1, 2, 2, Lq, Lk, 64, torch.bfloat16, 11, cuda)
+        q, k = q * 2.0 ** 33, k * 2.0 ** 33
+        for kw in (dict(), dict(causal=True), dict(bias=torch.full((2, 9), 3.0, device=cuda))):
+            kw = dict(kw, cap=1e30)
+            _check(sdk.sd_attention_masked(q, k, v, **kw), q, k, v, **kw)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("ahead", [20.0, -20.0])
+@pytest.mark.parametrize("cap", [30.0, 1e4, 1e6, 1e7])
+def test_the_cap_of_scores_of_its_size(cuda, cap, ahead, dtype):
+    # Two keys with scores of 0.45 and 0.225 of the cap, which a bias leaves 20 apart: the one ahead has all the
+    # weight. A score is off by 2e-7 of the cap and the bias by half a step of it: at 1e7 3 together.
+    t = TYPES[dtype]
+    q, k = torch.zeros(1, 1, 1, 64, dtype=t, device=cuda), torch.zeros(1, 1, 2, 64, dtype=t, device=cuda)
+    q[..., 0], k[0, 0, 0, 0], k[0, 0, 1, 0] = 4800.0, 12032.0, 6016.0
+    scale = cap * 0.45 / (4800.0 * 12032.0)
+    v = torch.randn(1, 1, 2, 64, generator=torch.Generator().manual_seed(12)).to(t).to(cuda)
+    apart = cap * (np.tanh(0.45) - np.tanh(0.225))
+    bias = torch.tensor([[-apart + ahead, 0.0, 0.0]], dtype=torch.float32, device=cuda)
+    o = sdk.sd_attention_masked(q, k, v, scale=scale, cap=cap, bias=bias)
+    sdk.sd_device_status()
+    assert torch.equal(o[0, 0, 0], v[0, 0, 0 if ahead > 0 else 1])

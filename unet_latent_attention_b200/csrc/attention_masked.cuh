@@ -70,6 +70,8 @@ struct Params {
   int planes, plane_group;  // planes; planes whose items are mixed
   float scale_log2;      // scale * log2(e)
   float cap_in, cap_out; // scale / cap, cap log2(e)
+  float cap_scale, cap_inv;  // scale, 1 / cap
+  int cap_raw;           // whether the cap's polynomial in q.k is within fp32
   unsigned int* err;
 };
 
@@ -238,14 +240,14 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// cap * log2(e) * tanh(x k) of one score, from two results of the special-function unit: off by 2e-7 of the
-// cap, which only a score of its size can bear.
-__device__ __forceinline__ float cap_large_score(float x, float k, float cap_log2) {
-  return fmaf(-2.f * cap_log2, rcp_approx(1.f + ex2_approx(x * (k * 2.885390081777927f))), cap_log2);
+// cap * log2(e) * tanh(u) from two results of the special-function unit: off by 2e-7 of the cap, which only a
+// score of its size can bear.
+__device__ __forceinline__ float cap_large_score(float u, float cap_log2) {
+  return fmaf(-2.f * cap_log2, rcp_approx(1.f + ex2_approx(u * 2.885390081777927f)), cap_log2);
 }
 
-// The same for |x k| <= 1/2 by an odd polynomial in x (coefficients from
-// unet_latent_attention_b200/fit_tanh_poly.py): off by 2e-7 of the score.
+// The same for |u| <= 1/2 by an odd polynomial (coefficients from unet_latent_attention_b200/fit_tanh_poly.py),
+// off by 2e-7 of the score: for u = x k, a polynomial in x = q.k.
 struct CapPoly {
   float2 c0, c1, c2, c3;  // twice each, for packed operations
 };
@@ -254,16 +256,24 @@ __device__ __forceinline__ CapPoly cap_poly(float k, float cap_log2) {
   const float2 c0 = {9.999976754e-01f * a0, 9.999976754e-01f * a0}, c1 = {-3.332065642e-01f * a1, -3.332065642e-01f * a1}, c2 = {1.314514577e-01f * a2, 1.314514577e-01f * a2}, c3 = {-4.337248206e-02f * a3, -4.337248206e-02f * a3};
   return {c0, c1, c2, c3};
 }
+__device__ __forceinline__ float cap_small_score(const CapPoly& c, float z, float v) {
+  return __fmul_rn(__fmaf_rn(__fmaf_rn(__fmaf_rn(c.c3.x, z, c.c2.x), z, c.c1.x), z, c.c0.x), v);
+}
 
-// One score by its own form, so that it does not depend on its neighbours' or on those of unseen keys.
-__device__ __forceinline__ float cap_score(float x, float k, float cap_log2) {
-  const CapPoly c = cap_poly(k, cap_log2);
-  const float z = __fmul_rn(x, x), p = __fmul_rn(__fmaf_rn(__fmaf_rn(__fmaf_rn(c.c3.x, z, c.c2.x), z, c.c1.x), z, c.c0.x), x);
-  return fabsf(x) * k > 0.5f ? cap_large_score(x, k, cap_log2) : p;
+// One score by its own form, so that it does not depend on its neighbours' or on those of unseen keys. Far from
+// ordinary caps (k^7 below fp32's range, where x^2 may pass it) the polynomial is one in u.
+__device__ __forceinline__ float cap_score(const Params& p, float x) {
+  if (p.cap_raw) {
+    if (fabsf(x) * p.cap_in > 0.5f) return cap_large_score(x * p.cap_in, p.cap_out);
+    return cap_small_score(cap_poly(p.cap_in, p.cap_out), __fmul_rn(x, x), x);
+  }
+  const float t = x * p.cap_scale, u = t * p.cap_inv;
+  if (fabsf(u) > 0.5f) return cap_large_score(u, p.cap_out);
+  return cap_small_score(cap_poly(1.f, 1.4426950408889634f), u * u, t);
 }
 
 // N scores, if all of the warp's are small (they stay below their cap by design), with the results of
-// cap_score: 5 packed operations for two values on the FMA pipe; the softmax needs the special-function unit
+// cap_score (cap_raw): 5 packed operations for two values on the FMA pipe; the softmax needs the special-function unit
 // for itself ([2, 10, 4096, 64]: 223 us; 332 us with cap_large_score alone). False, with nothing done, if a score
 // of the warp lies beyond.
 template <int N>
@@ -608,7 +618,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         // instruction cache's way), in units of log2: large scores under a cap, and a bias over documents
         // with different shifts, where each row has its own distances.
         bool slow = is_mixed;
-        if constexpr (C::CAP) slow = slow || !cap_small_scores(sv, p.cap_in, p.cap_out);
+        if constexpr (C::CAP) slow = slow || !p.cap_raw || !cap_small_scores(sv, p.cap_in, p.cap_out);
         if (slow) {
           const float* table = p.bias + static_cast<long long>(h0) * (2LL * p.radius + 1) + p.radius;
           const long long d = static_cast<long long>(j) * BN - (q_first + r_in) + me.shift;
@@ -620,7 +630,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float x = __uint_as_float(r[i]);
-              if (C::CAP) x = cap_score(x, p.cap_in, p.cap_out);
+              if (C::CAP) x = cap_score(p, x);
               if (C::BIAS && is_mixed)
                 x = fmaf(x, C::CAP ? 1.f : p.scale_log2, bias_log2(__ldg(table + clampll(d + c * 16 + i, -p.radius, p.radius))));
               r[i] = __float_as_uint(x);

@@ -47,6 +47,12 @@ sd_status launch(const Launch& l, int pack, int64_t tiles, int splits) {
   p.scale_log2 = std::min(std::max(a.scale * kLog2e, 1.17549435e-38f), 3.402823466e38f);
   p.cap_in = C::CAP ? a.scale / a.cap : 0.f;
   p.cap_out = a.cap * kLog2e;
+  if (C::CAP) {
+    p.cap_scale = a.scale, p.cap_inv = 1.f / a.cap;
+    // The smallest coefficient of the polynomial in q.k, cap k^7 log2(e) / 23, has to keep its 24 bits.
+    const float k = p.cap_in, least = std::min(1.f, k * k * k * k * k * k) * p.cap_out * k / 23.f;
+    p.cap_raw = least >= 1.17549435e-38f;
+  }
   p.err = sd::device_status_word();
   if (!p.err) return SD_ERR_CUDA;
 
