@@ -323,7 +323,9 @@ sd_status sd_rope_axes(const sd_rope_args* args, void* stream);
  *   key j is seen if j < len_s and (not causal, or j <= p, or j < prefix_s);
  *   o_i = sum_j softmax_j(t_ij over the seen keys) v_j, and 0 where no key is seen (or every seen
  *   t_ij is -infinity).
- * Values of keys that a query does not see have no influence on it, infinities and NaN included.
+ * Values of keys that a query does not see have no influence on it, infinities and NaN included. Infinities
+ *   and NaN of a seen key whose weight is 0 (a bias of -infinity, a score far below the row's largest) may or
+ *   may not reach the row.
  * Batched (offsets NULL): sequence s is batch row s with all Lq queries; len_s = kv_lens[s] or Lk;
  *   start_s = q_starts[s] or Lk - Lq.
  * Packed documents (B = 1, q_offsets and k_offsets given, kv_lens NULL): document s has the queries

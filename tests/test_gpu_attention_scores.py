@@ -166,3 +166,20 @@ def test_the_cap_of_scores_of_its_size(cuda, cap, ahead, dtype):
     o = sdk.sd_attention_masked(q, k, v, scale=scale, cap=cap, bias=bias)
     sdk.sd_device_status()
     assert torch.equal(o[0, 0, 0], v[0, 0, 0 if ahead > 0 else 1])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("Lq,Lk", [(150, 150), (2, 2000)])
+def test_rows_of_minus_infinity_are_zero_beside_infinite_values(cuda, Lq, Lk, dtype):
+    # the last row sees keys with a bias of -infinity only, one of them with an infinite and a NaN value
+    q, k, v = _whole_numbers(1, 2, 2, Lq, Lk, 64, TYPES[dtype], 13, cuda)
+    d = torch.arange(-Lk, Lk + 1, device=cuda)
+    bias = torch.where(d == Lk - Lq + 1, 0.0, float("-inf")).expand(2, -1).contiguous()  # key i + 1 + Lk - Lq of row i
+    starts = _ints([0], cuda)
+    want = sdk.sd_attention_masked(q, k, v, bias=bias, q_starts=starts)
+    v[:, :, Lk - 3, 3], v[:, :, Lk - 3, 5] = float("inf"), float("nan")
+    o = sdk.sd_attention_masked(q, k, v, bias=bias, q_starts=starts)
+    sdk.sd_device_status()
+    assert (want[:, :, -1] == 0).all() and (o[:, :, -1] == 0).all()
+    fine = [c for c in range(64) if c not in (3, 5)]
+    assert torch.equal(o[..., fine], want[..., fine])

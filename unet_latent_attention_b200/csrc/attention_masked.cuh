@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = l_run == 0.f ? 0.f : __uint_as_float(r[i]) * inv;
-          if (fix && store) add_cleaned(c * 16, o);
+          if (fix && store && l_run != 0.f) add_cleaned(c * 16, o);  // every seen score -infinity: 0 all the same
         } else {
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i] = 0.f;
