@@ -168,3 +168,19 @@ def test_the_cap_polynomial_is_the_fitted_one():
     # the source holds them rounded to fp32: off by half a step, 2^-24 of the value, at most
     assert len(used) == len(c) == 4 and all(abs(a - b) <= 2.0 ** -24 * abs(b) for a, b in zip(used, c))
     assert err < 1.5e-7 and fit_tanh_poly.error_f32(c) < 2e-7
+
+
+def test_rope_views_that_share_an_element_are_refused(L):
+    # q [2, 2, 4, 64] (batch, heads, tokens, columns) in a buffer of five heads a batch, bf16, in place; k anywhere in it
+    def views(k_out):
+        h, b = 4 * 64, 5 * 4 * 64
+        a = {}
+        for t in ("qs", "ks", "qos", "kos"):
+            a.update({f"{t}0": b, f"{t}1": 64, f"{t}2": h})
+        return _rope(L, B=2, q=P, q_out=P, k=P + (1 << 16), k_out=k_out, **a)
+    heads = [P + 2 * 4 * 64 * h for h in range(-5, 5)]
+    for h in (-5, -4, 0, 1):  # a head of q, of this batch or the next
+        assert views(heads[h + 5]) == 1
+    for shift in (16, 2 * 64, -16):  # between two heads
+        assert views(heads[5] + shift) == 1 and views(heads[6] + shift) == 1
+    assert views(heads[7] - 16) == 1 and views(heads[4] + 16) == 1

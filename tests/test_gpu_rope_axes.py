@@ -199,3 +199,41 @@ def test_refusals(cuda):
     with pytest.raises(sdk.SDError, match="heads overlap"):
         sdk.sd_rope_axes(q, None, pos, f, axes, q_out=torch.zeros(1, 8, 1, 64, device=cuda).expand(1, 8, 2, 64))
     assert sdk.sd_rope_axes(q[:, :0], None, pos[:0], f, axes)[0].shape == (1, 0, 2, 64)
+
+
+def _fused(name, B, L, H, KV, dh, t, dev):
+    """(buffer, q, k, layout, the rest): q and k as slices of one buffer that step over one another."""
+    g = torch.Generator().manual_seed(31)
+    if name == "heads first":  # [B, heads, L, dh]: the batches of q and k alternate
+        buf = torch.randn(B, H + 2 * KV, L, dh, generator=g).to(t).to(dev)
+        return buf, buf[:, :H], buf[:, H:H + KV], "bhld", buf[:, H + KV:]
+    if name == "by head":  # [B, L, heads, 3, dh]: the heads of q and k alternate
+        buf = torch.randn(B, L, KV, 3, dh, generator=g).to(t).to(dev)
+        return buf, buf[:, :, :, 0], buf[:, :, :, 1], "blhd", buf[:, :, :, 2]
+    if name == "by token":  # [L, B, heads, dh], the tokens' rows outermost
+        buf = torch.randn(L, B, H + 2 * KV, dh, generator=g).to(t).to(dev)
+        x = buf.transpose(0, 1)
+        return buf, x[:, :, :H], x[:, :, H:H + KV], "blhd", x[:, :, H + KV:]
+    buf = torch.randn(B, L, H + KV, 2 * dh, generator=g).to(t).to(dev)  # columns of wider heads
+    return buf, buf[:, :, :H, :dh], buf[:, :, H:, dh:], "blhd", torch.cat((buf[:, :, :H, dh:], buf[:, :, H:, :dh]), 2)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("B", [1, 3])
+@pytest.mark.parametrize("name", ["heads first", "by head", "by token", "wide heads"])
+def test_in_place_on_slices_of_one_buffer(cuda, name, B, dtype):
+    axes, L, H, KV, dh = (16, 24, 24), 21, 4, 2, 64
+    buf, q, k, layout, rest = _fused(name, B, L, H, KV, dh, TYPES[dtype], cuda)
+    pos = torch.randint(0, 64, (B, L, 3), generator=torch.Generator().manual_seed(32), dtype=torch.int32).to(cuda)
+    freqs = sdk.rope_frequencies(axes)
+    before = rest.clone()
+    qo, ko = sdk.sd_rope_axes(q, k, pos, freqs, axes, layout=layout)
+    first = (lambda x: x) if layout == "blhd" else (lambda x: x.transpose(1, 2))
+    _check(first(qo), first(q), pos, freqs, axes, False, None)
+    _check(first(ko), first(k), pos, freqs, axes, False, None)
+    sdk.sd_rope_axes(q, k, pos, freqs, axes, layout=layout, q_out=q, k_out=k)
+    assert torch.equal(q, qo) and torch.equal(k, ko)
+    buf2, q2, k2, _, rest2 = _fused(name, B, L, H, KV, dh, TYPES[dtype], cuda)
+    assert torch.equal(before, rest2)
+    q2.copy_(qo), k2.copy_(ko)
+    assert torch.equal(buf, buf2)  # nothing else was written

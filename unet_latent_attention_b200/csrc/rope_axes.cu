@@ -326,13 +326,6 @@ struct View {
     for (int i = 0; i < 3; ++i) last += (n[i] - 1) * stride[i];
     return last * size;
   }
-  // One row per token, if the tokens lie on one lattice (those between the batches' included).
-  bool as_rows(sd::rows::RowSpan* r) const {
-    const int64_t step = n[1] > 1 ? stride[1] : stride[0];
-    if (n[0] * n[1] <= 1 || step <= 0 || (n[0] > 1 && stride[0] % step)) return false;
-    *r = {ptr, step * size, ((n[2] - 1) * stride[2] + dh) * size};
-    return r->stride >= r->bytes;
-  }
   // Whether two of its heads share an element.
   bool folds() const {
     int order[3] = {0, 1, 2};
@@ -347,14 +340,42 @@ struct View {
   }
 };
 
-// Views with the rows of one buffer (a fused projection's q and k) are compared row by row, others
-// by their extents.
+// A dimension of two views: bytes from one element to the next, and how many elements each has.
+struct Step {
+  int64_t bytes, na, nb;
+};
+
+// Whether a head of one view and a head of another `d` bytes behind it meet, each moved along the first `n`
+// steps. Steps contain one another (meet), so along the largest only two places come near.
+bool heads_meet(int64_t d, const Step* step, int n, int64_t head) {
+  if (n == 0) return d < head && -d < head;
+  const Step& s = step[n - 1];
+  const int64_t near = d / s.bytes + (d % s.bytes > 0);  // of the first view, counted from the second
+  for (int64_t t : {near, near - 1})
+    if (t < s.na && -t < s.nb && heads_meet(d - t * s.bytes, step, n - 1, head)) return true;
+  return false;
+}
+
+// Whether two views share an element: exactly, where they step alike and no step of theirs is within a smaller
+// one (q and k in one buffer, in any layout); others by their extents.
 bool meet(const View& a, const View& b) {
-  sd::rows::RowSpan ra, rb;
   if (!sd::overlaps(a.ptr, a.bytes(), b.ptr, b.bytes())) return false;
-  if (!a.as_rows(&ra) || !b.as_rows(&rb) || ra.stride != rb.stride) return true;
-  const int64_t rows = (std::max(a.bytes(), b.bytes()) + ra.stride - 1) / ra.stride;
-  return sd::rows::overlap(ra, rb, rows);
+  Step step[3];
+  int n = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (a.n[i] <= 1 && b.n[i] <= 1) continue;
+    if (a.n[i] > 1 && b.n[i] > 1 && a.stride[i] != b.stride[i]) return true;
+    step[n++] = {(a.n[i] > 1 ? a.stride[i] : b.stride[i]) * a.size, a.n[i], b.n[i]};
+  }
+  std::sort(step, step + n, [](const Step& x, const Step& y) { return x.bytes < y.bytes; });
+  const int64_t head = a.dh * a.size;
+  int64_t span_a = head, span_b = head;
+  for (int i = 0; i < n; ++i) {
+    if (step[i].bytes < span_a || step[i].bytes < span_b) return true;
+    span_a += (step[i].na - 1) * step[i].bytes;
+    span_b += (step[i].nb - 1) * step[i].bytes;
+  }
+  return heads_meet(static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.ptr) - reinterpret_cast<uintptr_t>(a.ptr)), step, n, head);
 }
 
 sd_status check_view(const char* name, const View& v, bool output) {
