@@ -243,8 +243,8 @@ sd_status sd_cfg_dpmpp_3m_step(const float* x, const float* eps_u, const float* 
  * RMS norm of rows with the residual's addition: for each of `rows` rows of `cols` values
  *   h = x + residual (x where residual is NULL), in fp32,
  *   residual_out = h rounded to the type,   y = h * rsqrt(mean(h^2) + eps) * weight
- * y is formed from the unrounded h and rounded once. Squares are summed in fp32 (magnitudes above 1e19
- * overflow them).
+ * y is formed from the unrounded h and rounded once. A row's squares have to sum to less than 3.4e38, and
+ * with eps = 0 to more than 1e-37, the range of fp32; at any width the sum is off by 6e-6 of itself at most.
  *  dtype  : of x, residual, residual_out and y: 0 = bf16, 1 = fp16, 2 = fp32.
  *  weight : [cols], fp32 (weight_f32 = 1) or of the type dtype (weight_f32 = 0); NULL = ones.
  *  residual, residual_out : may be NULL; residual_out needs residual.

@@ -162,3 +162,25 @@ def test_captured_and_on_another_stream(cuda):
     for a, b in zip(out, want):
         assert torch.equal(a.view(torch.uint8) if a.dtype == torch.float8_e4m3fn else a,
                            b.view(torch.uint8) if b.dtype == torch.float8_e4m3fn else b)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("C", [1 << 24, (1 << 22) + 7])
+def test_wide_rows_of_equal_values(cuda, C, dtype):
+    # equal terms round the same way at every addition: a long chain of them drifts
+    t = TYPES[dtype]
+    for value in (1.1, 3.3):
+        x = torch.full((1, C), value, dtype=t, device=cuda)
+        v = float(x[0, 0])
+        want = v / np.sqrt(v * v + 1e-6)
+        y = sdk.sd_rms_norm(x)
+        assert ((y.double() - want).abs() <= want * (_half_step(t) + ARITH)).all()
+        q, s = sdk.sd_rms_norm_fp8(x, block=0)
+        assert (q.float() == 448).all() and abs(float(s) - want / 448) <= 2 * ARITH * want / 448
+        x[0, ::2] *= 2
+        a, b = float(x[0, 0]), v
+        n = (C + 1) // 2
+        rms = np.sqrt((n * a * a + (C - n) * b * b) / C + 1e-6)
+        y, h = sdk.sd_rms_norm(x, residual=torch.zeros_like(x))
+        assert ((y[0, ::2].double() - a / rms).abs() <= a / rms * (_half_step(t) + ARITH)).all() and torch.equal(h, x)
+        assert ((y[0, 1::2].double() - b / rms).abs() <= b / rms * (_half_step(t) + ARITH)).all()

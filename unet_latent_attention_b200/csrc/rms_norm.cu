@@ -285,19 +285,23 @@ __global__ void __launch_bounds__(kMaxThreads) rms_norm_kernel(const RmsArgs a, 
     }
   } else {
     const int chunk = row_threads * PACK;  // columns that the row's threads take at a time
-    float ss = 0.f, row_top = 0.f;
+    // A thread adds up to 2^19 packs: in fp32 the roundings of equal terms would all point one way (2e-4 at 2^24
+    // columns of 1.1), so the packs' sums are added in fp64.
+    double packs = 0.0;
+    float row_top = 0.f;
     for (int i = 0; static_cast<long long>(i) * chunk < a.cols; ++i) {
-      float h[PACK];
+      float h[PACK], ss = 0.f;
       read(i * row_threads + tid, h);
 #pragma unroll
       for (int e = 0; e < PACK; ++e) ss = fmaf(h[e], h[e], ss);
+      packs += ss;
       if (FP8 && a.block == 0) {
         weighted(i * row_threads + tid, h);
 #pragma unroll
         for (int e = 0; e < PACK; ++e) row_top = max_nan(row_top, fabsf(h[e]));
       }
     }
-    const Totals t = row_totals<FP8>(ss, row_top, warp_row, part);
+    const Totals t = row_totals<FP8>(static_cast<float>(packs), row_top, warp_row, part);
     const float rstd = rstd_of(t.sum);
     if (FP8 && a.block == 0 && tid == 0) a.scales[row] = scale_of(t.top, rstd);
     for (int i = 0; static_cast<long long>(i) * chunk < a.cols; ++i) {
