@@ -183,3 +183,15 @@ def test_rows_of_minus_infinity_are_zero_beside_infinite_values(cuda, Lq, Lk, dt
     assert (want[:, :, -1] == 0).all() and (o[:, :, -1] == 0).all()
     fine = [c for c in range(64) if c not in (3, 5)]
     assert torch.equal(o[..., fine], want[..., fine])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("dh", [8, 40, 64, 80, 128, 160])
+@pytest.mark.parametrize("Lq,Lk", [(1, 1), (5, 2050), (200, 333)])
+def test_ordinary_scores(cuda, dh, Lq, Lk, dtype):
+    # with exact products nothing but the weights' own roundings is left
+    q, k, v = _whole_numbers(2, 4, 2, Lq, Lk, dh, TYPES[dtype], 14 + dh, cuda)
+    lens, starts = _ints([Lk, Lk // 3], cuda), _ints([Lk - Lq, 0], cuda)
+    bias = torch.randn(4, 61, generator=torch.Generator().manual_seed(15)).to(cuda)
+    for kw in (dict(), dict(causal=True, kv_lens=lens, q_starts=starts), dict(cap=30.0, kv_lens=lens), dict(bias=bias), dict(bias=bias, cap=9.0, causal=True)):
+        _check(sdk.sd_attention_masked(q, k, v, **kw), q, k, v, **kw)
