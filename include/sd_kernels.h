@@ -107,6 +107,8 @@ sd_status sd_group_norm_silu(const float* x, const float* gamma, const float* be
  *  k, v   : bf16 [B, heads, Lk, dh] contiguous (self-attention: Lk = Lq = H*W;
  *           cross-attention: Lk = 77 text tokens, already projected to heads x dh).
  *  o      : bf16 [B, heads, Lq, dh] contiguous; must not overlap q, k or v.
+ *  Scores |scale * q.k| have to stay below 2^24: a score and its row's maximum are rounded apart, and from
+ *           about 2^27 on the difference leaves exp2's range (sd_attention_masked takes any score).
  *  dh     : one of 40, 64, 80, 160 (SD1.5 and SDXL head sizes); others are SD_ERR_UNSUPPORTED.
  *  scale  : finite and >= 0 (SD_ERR_INVALID_ARG if not finite, SD_ERR_UNSUPPORTED if negative);
  *           callers normally pass 1/sqrt(dh).
@@ -280,7 +282,8 @@ sd_status sd_rms_norm_fp8(const void* x, const void* residual, const void* weigh
  *   y = x * rsqrt(mean(x^2) + eps) * weight     (y = x where the weight is NULL), in fp32,
  * and pair m of the axis a that holds it, (u, v) -> (u cos - v sin, u sin + v cos) with the angle
  *   2 pi * frac(positions[b, t, a] * freqs[m] / 2^64),
- * rounded once. Columns behind the axes' columns are normalised but not turned. With -freqs the
+ * rounded once. Columns behind the axes' columns are normalised but not turned. A normalised head's squares
+ * have to sum to less than 3.4e38, and with eps = 0 to more than 1e-37. With -freqs the
  * rotation is undone, which is also its gradient's form.
  *  q, k, q_out, k_out : [B, L, heads, dh] and [B, L, kv_heads, dh] views of the type dtype (0 = bf16,
  *           1 = fp16, 2 = fp32) with strides {batch, token, head} in elements and contiguous columns,
@@ -340,6 +343,8 @@ sd_status sd_rope_axes(const sd_rope_args* args, void* stream);
  *           h / (heads / kv_heads); kv_heads divides heads. o must not overlap q, k or v (the
  *           views' extents are compared), nor fold onto itself.
  *  dh     : a multiple of 8 from 8 to 160.  Lq, Lk < 2^30, B * heads < 2^31. Lk = 0 gives zeros.
+ * Scores, their maximum and the sum of weights are held in fp32. The weights are rounded to the inputs' type
+ *   for the product with v: half a step each, and in fp16 weights below 2^-25 of the largest may become 0 there.
  * The sums q.k have to stay within fp32, with a bias and no cap also the scores (times log2(e)); within that
  *   scores may be of any size.
  *  scale  : finite and >= 0.  cap: 0 = none, else in [1e-6, 1e30], with scale / cap below 1e5.

@@ -21,7 +21,7 @@
 //    running maximum is raised only when it grows by more than 2^8.
 // Two CTAs share an SM (up to 128 columns): while one waits for S, P V or a copy, the other has the
 // special-function unit, and one's start and end hide behind the other's tiles. No waiting is shared
-// between them, so items of any length mix. Measured for [2, 10, 4096, 64] and [2, 8, 4096, 128]: 148 and 139
+// between them, so items of any length mix. Measured for [2, 10, 4096, 64] and [2, 8, 4096, 128]: 146 and 141
 // us; two query tiles in one CTA, with turns on the special-function unit, 192 and 187; eight softmax
 // warps on half rows 193 and 164 with one CTA an SM, 160 at 64 columns with two.
 //

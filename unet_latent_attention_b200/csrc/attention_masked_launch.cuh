@@ -37,7 +37,7 @@ sd_status launch(const Launch& l, int pack, int64_t tiles, int splits) {
   p.tiles = static_cast<int>(tiles);
   p.planes = static_cast<int>(a.B * (a.heads / pack));
   // Where items differ in length, as many planes are mixed as have 48 MB of keys and values, under half of
-  // L2 (causal [2, 10, 4096, 64]: 77 us with all 20 planes mixed, 106 one after the other).
+  // L2 (causal [2, 10, 4096, 64]: 74 us; beside 77 at the time 106 with one plane after the other).
   const int64_t plane_bytes = std::max<int64_t>(a.Lk * a.dh * 4 * pack / l.group, 1);
   p.plane_group = a.causal || a.q_offsets || a.kv_lens
                       ? static_cast<int>(std::min<int64_t>(std::max<int64_t>((int64_t(48) << 20) / plane_bytes, 1), p.planes))
@@ -98,7 +98,7 @@ sd_status choose(const Launch& l) {
   // Idle SMs: split the keys over a cluster, two key tiles a CTA at least, while all clusters run at once.
   // (Beyond that the clusters' starts, joins and ends cost more than they even out: B200, [32, 16, 1, 2048
   // ragged, 64] takes 52, 61, 91 and 167 us with 1, 2, 4 and 8 parts; [4, 32 / 8 heads, 1, 16384, 128] 232, 122, 68 and 49;
-  // [16, 16 / 4 heads, 1, 8192 ragged, 128] 39 with 4 parts and 46 with 8.)
+  // [16, 16 / 4 heads, 1, 8192 ragged, 128] 40 with 4 parts and, beside 39 at the time, 46 with 8.)
   int splits = 1;
   const int64_t key_tiles = (a.Lk + C::BN - 1) / C::BN;
   while (2 * splits <= kMaxSplits && planes * tiles * 2 * splits <= C::CTAS * sd::sm_count() && key_tiles >= 4 * splits) splits *= 2;
