@@ -290,8 +290,8 @@ sd_status sd_rms_norm_fp8(const void* x, const void* residual, const void* weigh
  *           so that both layouts of sd_attention and the rows of a fused projection will do; 16-byte
  *           aligned, strides multiples of 16 bytes (SD_ERR_MISALIGNED). heads or kv_heads may be 0:
  *           that tensor is then not looked at. q_out may be q and k_out may be k exactly (in place);
- *           any other overlap of an output is SD_ERR_INVALID_ARG (views of equal strides, such as slices of
- *           one buffer, are compared element by element, others by their extents).
+ *           any other overlap of an output is SD_ERR_INVALID_ARG (dimensions of equal strides, as of slices of
+ *           one buffer, are compared place by place, others by their extents).
  *  dh     : a multiple of 8 from 8 to 256.
  *  axes, axis_dims : 1 to 4 axes of an even number of columns each (0 allowed), together a multiple of
  *           8 and at most dh. Axis a holds the pairs behind those of axis a - 1.

@@ -195,3 +195,27 @@ def test_ordinary_scores(cuda, dh, Lq, Lk, dtype):
     bias = torch.randn(4, 61, generator=torch.Generator().manual_seed(15)).to(cuda)
     for kw in (dict(), dict(causal=True, kv_lens=lens, q_starts=starts), dict(cap=30.0, kv_lens=lens), dict(bias=bias), dict(bias=bias, cap=9.0, causal=True)):
         _check(sdk.sd_attention_masked(q, k, v, **kw), q, k, v, **kw)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("scale", [0.125, 1e9])
+@pytest.mark.parametrize("Lq,Lk", [(150, 400), (1, 3000)])
+def test_large_scores_beside_unseen_values(cuda, Lq, Lk, scale, dtype):
+    # infinities and NaN behind the lengths, and seen keys with a score of -infinity, whatever form the row takes
+    t = TYPES[dtype]
+    for dh in (64, 128):
+        q, k, v = _whole_numbers(2, 4, 2, Lq, Lk, dh, t, 16 + dh, cuda)
+        lens = _ints([Lk - 10, Lk // 3], cuda)
+        for kw in (dict(), dict(bias=torch.full((4, 5), -2.0, device=cuda))):
+            kw = dict(kw, scale=scale, kv_lens=lens)
+            want = sdk.sd_attention_masked(q, k, v, **kw)
+            _check(want, q, k, v, **kw)
+            for x in (float("nan"), float("inf"), float("-inf"), torch.finfo(t).max):
+                k2, v2 = k.clone(), v.clone()
+                for b, n in enumerate(lens.tolist()):
+                    k2[b, :, n:], v2[b, :, n:] = x, x
+                assert torch.equal(sdk.sd_attention_masked(q, k2, v2, **kw), want), x
+        bias = torch.full((4, 2 * Lk + 1), 0.0, device=cuda)
+        bias[:, ::3] = float("-inf")
+        kw = dict(scale=scale, kv_lens=lens, bias=bias)
+        _check(sdk.sd_attention_masked(q, k, v, **kw), q, k, v, **kw)

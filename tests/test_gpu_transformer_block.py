@@ -128,3 +128,40 @@ def test_a_token_at_a_time_is_the_whole_sequence(cuda):
         a = sdk.sd_attention_masked(qi, kr[:, :i + 1].contiguous(), v[:, :i + 1].abs().contiguous(), layout="blhd").float()
         # both round each weight and the output: twice the tolerance of one
         assert ((o.float() - whole[:, i:i + 1].float()).abs() <= 4 * BF16 * (a * 1.01) + 1e-6).all()
+
+
+def test_offsets_beyond_32_bits(cuda):
+    # rows, batches and caches whose elements lie more than 2^32 apart, in one large buffer
+    far = (1 << 32) + 4096
+    big = torch.empty(far + (1 << 20), dtype=torch.bfloat16, device=cuda)
+    g = torch.Generator().manual_seed(8)
+
+    def spread(at, *shape):  # [2, ...], the second one `far` elements behind the first
+        n = int(np.prod(shape))
+        strides = [int(np.prod(shape[i + 1:])) for i in range(len(shape))]
+        x = big.as_strided((2, *shape), (far, *strides), at)
+        dense = torch.randn(2, *shape, generator=g).to(torch.bfloat16).to(cuda)
+        x.copy_(dense)
+        return x, dense, at + n
+
+    x, xd, at = spread(0, 1280)
+    out, _, at = spread(at, 1280)
+    w = 1 + 0.1 * torch.randn(1280, generator=g).to(cuda)
+    sdk.sd_rms_norm(x, w, out=out)
+    assert torch.equal(out, sdk.sd_rms_norm(xd, w))
+    q, qd, at = spread(at, 5, H, DH)
+    k, kd, at = spread(at, 300, KV, DH)
+    v, vd, at = spread(at, 300, KV, DH)
+    o = torch.empty(far + 5 * H * DH, dtype=torch.bfloat16, device=cuda).as_strided((2, 5, H, DH), (far, H * DH, DH, 1))
+    pos = torch.randint(0, 64, (2, 5, 3), generator=g, dtype=torch.int32).to(cuda)
+    f = sdk.rope_frequencies(AXES)
+    qo, ko = sdk.sd_rope_axes(qd, kd[:, :5], pos, f, AXES)
+    sdk.sd_rope_axes(q, k[:, :5], pos, f, AXES, q_out=q, k_out=k[:, :5])
+    assert torch.equal(q, qo) and torch.equal(k[:, :5], ko) and torch.equal(k[:, 5:], kd[:, 5:])
+    vd[:, 290, 1, 3] = float("inf")  # found again in v itself by the rows that see it
+    v.copy_(vd)
+    n = torch.tensor([295, 300], dtype=torch.int32, device=cuda)
+    sdk.sd_attention_masked(q, k, v, layout="blhd", causal=True, kv_lens=n, q_starts=n - 5, out=o)
+    want = sdk.sd_attention_masked(qo, torch.cat((ko, kd[:, 5:]), 1), vd, layout="blhd", causal=True, kv_lens=n, q_starts=n - 5)
+    sdk.sd_device_status()
+    assert torch.equal(o, want) and want.isinf().any() and not want.isnan().any()

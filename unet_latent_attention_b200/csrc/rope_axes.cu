@@ -345,37 +345,45 @@ struct Step {
   int64_t bytes, na, nb;
 };
 
-// Whether a head of one view and a head of another `d` bytes behind it meet, each moved along the first `n`
-// steps. Steps contain one another (meet), so along the largest only two places come near.
-bool heads_meet(int64_t d, const Step* step, int n, int64_t head) {
-  if (n == 0) return d < head && -d < head;
+// Whether a block of `block_a` bytes and one of `block_b` bytes, `d` bytes behind it, meet, each moved along the
+// first `n` steps. Steps contain one another (meet), so along the largest only two places come near.
+bool blocks_meet(int64_t d, const Step* step, int n, int64_t block_a, int64_t block_b) {
+  if (n == 0) return d < block_a && -d < block_b;
   const Step& s = step[n - 1];
   const int64_t near = d / s.bytes + (d % s.bytes > 0);  // of the first view, counted from the second
   for (int64_t t : {near, near - 1})
-    if (t < s.na && -t < s.nb && heads_meet(d - t * s.bytes, step, n - 1, head)) return true;
+    if (t < s.na && -t < s.nb && blocks_meet(d - t * s.bytes, step, n - 1, block_a, block_b)) return true;
   return false;
 }
 
-// Whether two views share an element: exactly, where they step alike and no step of theirs is within a smaller
-// one (q and k in one buffer, in any layout); others by their extents.
+// Whether two views share an element. Dimensions in which they step alike, each step past all within it, are
+// followed exactly (q and k in one buffer, in any layout); what lies within the others counts as one block.
 bool meet(const View& a, const View& b) {
   if (!sd::overlaps(a.ptr, a.bytes(), b.ptr, b.bytes())) return false;
+  int64_t block_a = a.dh * a.size, block_b = block_a;
   Step step[3];
   int n = 0;
   for (int i = 0; i < 3; ++i) {
-    if (a.n[i] <= 1 && b.n[i] <= 1) continue;
-    if (a.n[i] > 1 && b.n[i] > 1 && a.stride[i] != b.stride[i]) return true;
-    step[n++] = {(a.n[i] > 1 ? a.stride[i] : b.stride[i]) * a.size, a.n[i], b.n[i]};
+    if (a.n[i] > 1 && b.n[i] > 1 && a.stride[i] != b.stride[i]) {
+      block_a += (a.n[i] - 1) * a.stride[i] * a.size;
+      block_b += (b.n[i] - 1) * b.stride[i] * b.size;
+    } else if (a.n[i] > 1 || b.n[i] > 1) {
+      step[n++] = {(a.n[i] > 1 ? a.stride[i] : b.stride[i]) * a.size, a.n[i], b.n[i]};
+    }
   }
   std::sort(step, step + n, [](const Step& x, const Step& y) { return x.bytes < y.bytes; });
-  const int64_t head = a.dh * a.size;
-  int64_t span_a = head, span_b = head;
+  int64_t span_a = block_a, span_b = block_b;
+  int kept = 0;
   for (int i = 0; i < n; ++i) {
-    if (step[i].bytes < span_a || step[i].bytes < span_b) return true;
-    span_a += (step[i].na - 1) * step[i].bytes;
-    span_b += (step[i].nb - 1) * step[i].bytes;
+    const Step s = step[i];
+    const bool past = s.bytes >= span_a && s.bytes >= span_b;
+    span_a += (s.na - 1) * s.bytes;
+    span_b += (s.nb - 1) * s.bytes;
+    if (past) step[kept++] = s;
+    else kept = 0, block_a = span_a, block_b = span_b;
   }
-  return heads_meet(static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.ptr) - reinterpret_cast<uintptr_t>(a.ptr)), step, n, head);
+  const int64_t d = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b.ptr) - reinterpret_cast<uintptr_t>(a.ptr));
+  return blocks_meet(d, step, kept, block_a, block_b);
 }
 
 sd_status check_view(const char* name, const View& v, bool output) {
