@@ -240,10 +240,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// cap * log2(e) * tanh(u) from two results of the special-function unit: off by 2e-7 of the cap, which only a
-// score of its size can bear.
-__device__ __forceinline__ float cap_large_score(float u, float cap_log2) {
-  return fmaf(-2.f * cap_log2, rcp_approx(1.f + ex2_approx(u * 2.885390081777927f)), cap_log2);
+// cap * log2(e) * tanh(u) of two scores from two results of the special-function unit each: off by 2e-7 of the cap,
+// which only a score of its size can bear.
+__device__ __forceinline__ float2 cap_large_scores(float u0, float u1, float cap_log2) {
+  const float2 t = __fmul2_rn(make_float2(u0, u1), make_float2(2.885390081777927f, 2.885390081777927f));
+  const float2 e = __fadd2_rn(make_float2(ex2_approx(t.x), ex2_approx(t.y)), make_float2(1.f, 1.f));
+  return __ffma2_rn(make_float2(rcp_approx(e.x), rcp_approx(e.y)), make_float2(-2.f * cap_log2, -2.f * cap_log2),
+                    make_float2(cap_log2, cap_log2));
 }
 
 // The same for |u| <= 1/2 by an odd polynomial (coefficients from unet_latent_attention_b200/fit_tanh_poly.py),
@@ -256,26 +259,52 @@ __device__ __forceinline__ CapPoly cap_poly(float k, float cap_log2) {
   const float2 c0 = {9.999976754e-01f * a0, 9.999976754e-01f * a0}, c1 = {-3.332065642e-01f * a1, -3.332065642e-01f * a1}, c2 = {1.314514577e-01f * a2, 1.314514577e-01f * a2}, c3 = {-4.337248206e-02f * a3, -4.337248206e-02f * a3};
   return {c0, c1, c2, c3};
 }
-__device__ __forceinline__ float cap_small_score(const CapPoly& c, float z, float v) {
-  return __fmul_rn(__fmaf_rn(__fmaf_rn(__fmaf_rn(c.c3.x, z, c.c2.x), z, c.c1.x), z, c.c0.x), v);
+
+// What q.k = x becomes before the polynomial: v = x unit, u = v step; the score is v P(u^2), and |u| k <= 1/2 where
+// it is small. An ordinary cap has unit = step = 1. Far from it (scale / cap below 1e-7, where k^7 leaves fp32's
+// range and x^2 may pass it) v is the score without its cap, u = v / cap, k = 1.
+struct CapForm {
+  float unit, step, k, cap_log2;
+  CapPoly poly;
+};
+__device__ __forceinline__ CapForm cap_form(const Params& p) {
+  if (p.cap_raw) return {1.f, 1.f, p.cap_in, p.cap_out, cap_poly(p.cap_in, p.cap_out)};
+  return {p.cap_scale, p.cap_inv, 1.f, p.cap_out, cap_poly(1.f, 1.4426950408889634f)};
 }
 
-// One score by its own form, so that it does not depend on its neighbours' or on those of unseen keys. Far from
-// ordinary caps (k^7 below fp32's range, where x^2 may pass it) the polynomial is one in u.
-__device__ __forceinline__ float cap_score(const Params& p, float x) {
-  if (p.cap_raw) {
-    if (fabsf(x) * p.cap_in > 0.5f) return cap_large_score(x * p.cap_in, p.cap_out);
-    return cap_small_score(cap_poly(p.cap_in, p.cap_out), __fmul_rn(x, x), x);
+// N scores, each by the form of its own size, so that it does not depend on its neighbours' or on those of
+// unseen keys.
+template <int N>
+__device__ __forceinline__ void cap_scores(float (&x)[N], const CapForm& f) {
+  float u[N];
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 v = __fmul2_rn(make_float2(x[i], x[i + 1]), make_float2(f.unit, f.unit));
+    const float2 w = __fmul2_rn(v, make_float2(f.step, f.step)), z = __fmul2_rn(w, w);
+    float2 p = __ffma2_rn(f.poly.c3, z, f.poly.c2);
+    p = __ffma2_rn(p, z, f.poly.c1);
+    p = __ffma2_rn(p, z, f.poly.c0);
+    p = __fmul2_rn(p, v);
+    x[i] = p.x, x[i + 1] = p.y;
+    const float2 t = __fmul2_rn(w, make_float2(f.k, f.k));
+    u[i] = t.x, u[i + 1] = t.y;
+    any = any || fabsf(t.x) > 0.5f || fabsf(t.y) > 0.5f;
   }
-  const float t = x * p.cap_scale, u = t * p.cap_inv;
-  if (fabsf(u) > 0.5f) return cap_large_score(u, p.cap_out);
-  return cap_small_score(cap_poly(1.f, 1.4426950408889634f), u * u, t);
+  if (__any_sync(0xffffffffu, any)) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float2 y = cap_large_scores(u[i], u[i + 1], f.cap_log2);
+      x[i] = fabsf(u[i]) > 0.5f ? y.x : x[i];
+      x[i + 1] = fabsf(u[i + 1]) > 0.5f ? y.y : x[i + 1];
+    }
+  }
 }
 
 // N scores, if all of the warp's are small (they stay below their cap by design), with the results of
-// cap_score (cap_raw): 5 packed operations for two values on the FMA pipe; the softmax needs the special-function unit
-// for itself ([2, 10, 4096, 64]: 223 us; 332 us with cap_large_score alone). False, with nothing done, if a score
-// of the warp lies beyond.
+// cap_scores for an ordinary cap: 5 packed operations for two values on the FMA pipe; the softmax needs the
+// special-function unit for itself ([2, 10, 4096, 64]: 216 to 224 us; 454 where every tile has a score above half
+// the cap). False, with nothing done, if a score of the warp lies beyond.
 template <int N>
 __device__ __forceinline__ bool cap_small_scores(float (&x)[N], float k, float cap_log2) {
   float top[4] = {0.f, 0.f, 0.f, 0.f};
@@ -614,7 +643,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
       float scale = C::CAP ? 1.f : p.scale_log2, offset = 0.f;
       bool biased = false;
       if constexpr (C::CAP || C::BIAS) {
-        // The rare forms work on S in tensor memory, 16 columns at a time (a loop that stays out of the
+        // The rare forms work on S in tensor memory, 16 or 32 columns at a time (a loop that stays out of the
         // instruction cache's way), in units of log2: large scores under a cap, and a bias over documents
         // with different shifts, where each row has its own distances.
         bool slow = is_mixed;
@@ -622,20 +651,31 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         if (slow) {
           const float* table = p.bias + static_cast<long long>(h0) * (2LL * p.radius + 1) + p.radius;
           const long long d = static_cast<long long>(j) * BN - (q_first + r_in) + me.shift;
+          CapForm form{};
+          if constexpr (C::CAP) form = cap_form(p);
+          constexpr int W = C::CAP ? 32 : 16;
 #pragma unroll 1
-          for (int c = 0; c < BN / 16; ++c) {
-            uint32_t r[16];
-            tmem_ld16(tS + c * 16, r);
+          for (int c = 0; c < BN; c += W) {
+            uint32_t r[W];
+            float x[W];
+            if constexpr (W == 32) tmem_ld32(tS + c, r);
+            else tmem_ld16(tS + c, r);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float x = __uint_as_float(r[i]);
-              if (C::CAP) x = cap_score(p, x);
-              if (C::BIAS && is_mixed)
-                x = fmaf(x, C::CAP ? 1.f : p.scale_log2, bias_log2(__ldg(table + clampll(d + c * 16 + i, -p.radius, p.radius))));
-              r[i] = __float_as_uint(x);
+            for (int i = 0; i < W; ++i) x[i] = __uint_as_float(r[i]);
+            if constexpr (C::CAP) cap_scores(x, form);
+            if (C::BIAS && is_mixed) {
+#pragma unroll
+              for (int i = 0; i < W; ++i)
+                x[i] = fmaf(x[i], C::CAP ? 1.f : p.scale_log2, bias_log2(__ldg(table + clampll(d + c + i, -p.radius, p.radius))));
             }
-            tmem_st16(tS + c * 16, r);
+#pragma unroll
+            for (int h = 0; h < W; h += 16) {
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(x[h + i]);
+              tmem_st16(tS + c + h, w);
+            }
           }
           tmem_wait_st();
           load_scores();
