@@ -303,8 +303,7 @@ __device__ __forceinline__ void cap_scores(float (&x)[N], const CapForm& f) {
 
 // N scores, if all of the warp's are small (they stay below their cap by design), with the results of
 // cap_scores for an ordinary cap: 5 packed operations for two values on the FMA pipe; the softmax needs the
-// special-function unit for itself ([2, 10, 4096, 64]: 216 to 224 us; 454 where every tile has a score above half
-// the cap). False, with nothing done, if a score of the warp lies beyond.
+// special-function unit for itself ([2, 10, 4096, 64]: 216 us; 452 where every tile has a score above half the cap). False, with nothing done, if a score of the warp lies beyond.
 template <int N>
 __device__ __forceinline__ bool cap_small_scores(float (&x)[N], float k, float cap_log2) {
   float top[4] = {0.f, 0.f, 0.f, 0.f};
@@ -796,7 +795,7 @@ __global__ void __launch_bounds__(C::THREADS, C::CTAS)
         // first and is 0 for the largest score (of q.k, or of the sum with a bias as rounded to fp32). The check
         // costs 1 to 3% of short key tiles' time ([2, 8, 4096, 128]: 139 -> 141 us, one token of [16, 16 / 4, 8192
         // ragged, 128] 39.0 -> 40.0) and nothing of the long ones' ([2, 10, 4096, 64]: 146); done before exp2,
-        // where it waits for the maximum, 2 to 7%.
+        // where it waits for the maximum, 2 to 7%. Rows that take it: 319 us for [2, 10, 4096, 64].
         if (__any_sync(0xffffffffu, large)) {
           const int lo = me.lo - j * BN, hi = me.hi - j * BN;
           float sum = 0.f;
