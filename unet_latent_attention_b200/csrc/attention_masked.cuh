@@ -303,7 +303,8 @@ __device__ __forceinline__ void cap_scores(float (&x)[N], const CapForm& f) {
 
 // N scores, if all of the warp's are small (they stay below their cap by design), with the results of
 // cap_scores for an ordinary cap: 5 packed operations for two values on the FMA pipe; the softmax needs the
-// special-function unit for itself ([2, 10, 4096, 64]: 216 us; 452 where every tile has a score above half the cap). False, with nothing done, if a score of the warp lies beyond.
+// special-function unit for itself ([2, 10, 4096, 64]: 216 us; 452 where every tile has a score above half the
+// cap). False, with nothing done, if a score of the warp lies beyond.
 template <int N>
 __device__ __forceinline__ bool cap_small_scores(float (&x)[N], float k, float cap_log2) {
   float top[4] = {0.f, 0.f, 0.f, 0.f};
